@@ -265,6 +265,105 @@ QLORA_API int qlora_bwd_multi(const qlora_nf4_t* q, int n, const uint16_t* As, c
                               const uint16_t* dY, int64_t T, uint16_t* dX, float* dAs, float* dBs,
                               void* workspace, size_t workspace_bytes, qlora_stream_t stream);
 
+/* ------------------------------------------ many adapters at once (requests) */
+
+/*
+ * Many unmerged adapters beside one shared projection ([P2] "The LoRA
+ * hypothesis": one base in memory, a small adapter chosen per request).  Where
+ * qlora_fwd_multi takes a few adapters of one rank and an index per token,
+ * these calls take the requests of a batch (a length and an adapter each),
+ * ranks that differ, and thousands of adapters; a token costs its own
+ * adapter's rank only.
+ *
+ * The adapters of one linear are rows of two device matrices: A (rows x k)
+ * and B transposed (rows x d), both bf16.  Adapter a owns rows first[a] ..
+ * first[a] + rank[a] of both, and the rows up to the next multiple of 16
+ * ranks, which the caller keeps zero.  first, rank and scale (s_a = alpha_a /
+ * r_a) are device arrays of n entries; an entry whose rows do not lie in the
+ * pool, or whose rank exceeds `width`, counts as no adapter.  width: a
+ * multiple of 16, at least every rank, at most 256.  k % 8 == 0, d % 8 == 0,
+ * rows % 16 == 0.  Adapters whose gradients are taken must not share rows.
+ */
+typedef struct {
+  const uint16_t* A;
+  const uint16_t* Bt;
+  const int32_t* first;
+  const int32_t* rank;
+  const float* scale;
+  int64_t rows;
+  int64_t k;
+  int64_t d;
+  int32_t n;
+  int32_t width;
+} lora_pool_t;
+
+/*
+ * The maps of a batch of n_req requests over T rows and a pool of n adapters
+ * (device memory of the caller, 16-byte aligned; n_req and n at most 4096, T at
+ * most 2^22):
+ *   starts      n_req + 1: first row of each request, and the end of the last
+ *   idx         T: the token's adapter, -1 for none and behind the last request
+ *               (what qlora_fwd_multi takes)
+ *   order       T: the tokens grouped by adapter, ascending within a group,
+ *               those without an adapter last; -1 behind the last request
+ *   seg         n + 2: where each adapter's group starts in order, where the
+ *               group without an adapter starts, and the end
+ *   tile_first  n + 2, and tiles 4 * lora_requests_max_tiles(): the kernels'
+ *               work list
+ */
+typedef struct {
+  int32_t* starts;
+  int32_t* idx;
+  int32_t* order;
+  int32_t* seg;
+  int32_t* tile_first;
+  int32_t* tiles;
+  int64_t T;
+  int32_t n_req;
+  int32_t n;
+} lora_requests_t;
+
+/* Entries of the work list (0 for sizes outside the limits). */
+QLORA_API int64_t lora_requests_max_tiles(int n_req, int n, int64_t T);
+
+/*
+ * Fills `out`'s maps from the requests' lengths and adapters (device int32[n_req]
+ * each).  Request i takes the lens[i] rows behind those of request i - 1; a
+ * negative length counts as 0 and rows beyond T are cut off.  An adapter
+ * outside [0, n) means none.  The maps hold for every linear of the batch
+ * whose pool has n adapters.
+ */
+QLORA_API int lora_requests_plan(const int32_t* lens, const int32_t* adapters, const lora_requests_t* out,
+                                 qlora_stream_t stream);
+
+/*
+ * Y[t] = bf16(base[t] + s_a U[t] B_a^T), U[t] = X[t] A_a^T in fp32, a the
+ * adapter of token t; a token without one gets its base row.  X: T x k, base:
+ * T x d (bf16; NULL counts as zero), Y: T x d, may be `base` itself but
+ * must not overlap any input otherwise.  U_save: NULL, or T x width fp32, the
+ * token's U for the backward (zero beyond its rank).  Rows of Y and U_save
+ * behind the last request are left as they were.
+ */
+QLORA_API size_t lora_requests_fwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req);
+QLORA_API int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
+                                const uint16_t* base, uint16_t* Y, float* U_save, void* workspace,
+                                size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Backward with dL/dY = dY (T x d) and G[t] = dY[t] B_a:
+ *   dX[t] = bf16(base[t] + s_a G[t] A_a)   (base: the gradient through the
+ *           shared projection, T x k; NULL counts as zero; may be dX itself)
+ *   dA_a  = s_a sum_t G[t]^T X[t],   dBt_a = s_a sum_t U_saved[t]^T dY[t]
+ * over the adapter's tokens.  dA: rows x k, dBt: rows x d, fp32, overwritten in
+ * every adapter's rows: an adapter without tokens gets exact zeros, and so do
+ * the rows between its rank and the next multiple of 16.  Rows that no
+ * adapter owns are left as they were.  All sums are taken in a fixed order.
+ */
+QLORA_API size_t lora_requests_bwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req);
+QLORA_API int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
+                                const float* U_saved, const uint16_t* dY, const uint16_t* base, uint16_t* dX, float* dA,
+                                float* dBt, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
 /* ------------------------------------------- plain LoRA on a bf16 base */
 
 /*
@@ -309,6 +408,27 @@ QLORA_API int lora_bwd(const uint16_t* W, int64_t d, int64_t k, const uint16_t* 
 QLORA_API int lora_adam_step(float* master, uint16_t* weight_bf16, float* m, float* v, const float* grad,
                              int64_t n, int64_t step, float lr, float beta1, float beta2, float eps,
                              float weight_decay, qlora_stream_t stream);
+
+/*
+ * One step that orthogonalises the momentum (the Muon rule) on a stack of n
+ * matrices rows x cols, e.g. the A or B factors of several linears:
+ *   m = momentum m + grad;   u = nesterov ? grad + momentum m : m;
+ *   x = u / (|u|_F + eps), then `steps` times
+ *   x = a x + b (x x^T) x + c (x x^T)^2 x     (x^T for rows > cols);
+ *   master = (1 - lr weight_decay) master - lr scale x;
+ *   weight_bf16 = bf16_RN(master).
+ * `scale` is the caller's rule for the update's size (sqrt(max(1, rows/cols)),
+ * or 0.2 sqrt(max(rows, cols)) to match Adam's).  coefs: host array {a, b, c},
+ * or NULL for {3.4445, -4.7750, 2.0315}.  min(rows, cols) <= 256.  Arrays:
+ * device, n rows cols elements, 16-byte aligned, updated in place (grad is
+ * only read).  momentum in [0, 1), lr and weight_decay >= 0, eps > 0, 1 <=
+ * steps <= 16.  A zero u leaves only the decay.
+ */
+QLORA_API size_t lora_muon_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
+QLORA_API int lora_muon_step(float* master, uint16_t* weight_bf16, float* m, const float* grad, int64_t n, int64_t rows,
+                             int64_t cols, float lr, float momentum, int nesterov, float scale, float weight_decay,
+                             float eps, int steps, const float* coefs, void* workspace, size_t workspace_bytes,
+                             qlora_stream_t stream);
 
 /* ---------------------------------------------------------------- deploy */
 

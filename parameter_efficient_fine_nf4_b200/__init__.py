@@ -37,6 +37,18 @@ class _NF4(ctypes.Structure):
                 ("block", ctypes.c_int32), ("block2", ctypes.c_int32)]
 
 
+class _Pool(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("Bt", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("d", ctypes.c_int64), ("n", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
+class _Requests(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("order", ctypes.c_void_p),
+                ("seg", ctypes.c_void_p), ("tile_first", ctypes.c_void_p), ("tiles", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("n_req", ctypes.c_int32), ("n", ctypes.c_int32)]
+
+
 class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int64),
                 ("total_ms", ctypes.c_double), ("flops", ctypes.c_double),
@@ -51,6 +63,8 @@ _SIZE = ctypes.c_size_t
 _INT = ctypes.c_int
 _F = ctypes.c_float
 _NF4P = ctypes.POINTER(_NF4)
+_POOLP = ctypes.POINTER(_Pool)
+_REQP = ctypes.POINTER(_Requests)
 
 _SIGNATURES = {
     "qlora_strerror": (ctypes.c_char_p, [_INT]),
@@ -81,6 +95,15 @@ _SIGNATURES = {
     "lora_bwd": (_INT, [_VP, _I64, _I64, _VP, _VP, _INT, _F, _VP, _VP, _VP, _I64, _VP, _VP, _VP, _VP,
                         _SIZE, _VP]),
     "lora_adam_step": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _F, _F, _F, _F, _F, _VP]),
+    "lora_requests_max_tiles": (_I64, [_INT, _INT, _I64]),
+    "lora_requests_plan": (_INT, [_VP, _VP, _REQP, _VP]),
+    "lora_requests_fwd_workspace_bytes": (_SIZE, [_POOLP, _REQP]),
+    "lora_requests_fwd": (_INT, [_POOLP, _REQP, _VP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
+    "lora_requests_bwd_workspace_bytes": (_SIZE, [_POOLP, _REQP]),
+    "lora_requests_bwd": (_INT, [_POOLP, _REQP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
+    "lora_muon_workspace_bytes": (_SIZE, [_I64, _I64, _I64]),
+    "lora_muon_step": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _F, _F, _INT, _F, _F, _F, _INT, _VP, _VP, _SIZE,
+                              _VP]),
     "lora_merge_workspace_bytes": (_SIZE, [_I64, _I64, _INT]),
     "lora_merge": (_INT, [_NF4P, _VP, _VP, _INT, _F, _VP, _VP, _SIZE, _VP]),
     "lora_unmerge": (_INT, [_VP, _VP, _VP, _INT, _F, _I64, _I64, _VP, _VP, _SIZE, _VP]),
@@ -501,6 +524,260 @@ def lora_adam_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Ten
     _check(lib().lora_adam_step(_ptr(master), _ptr(weight_bf16), _ptr(m), _ptr(v), _ptr(grad), n, int(step),
                                 float(lr), float(beta1), float(beta2), float(eps), float(weight_decay),
                                 _stream(stream)), "lora_adam_step")
+
+
+# ------------------------------------------------- many adapters at once (requests)
+class _On:
+    """The device a call runs on: makes it current, allocates on the call's
+    stream (so that a temporary's memory is reused in that stream's order) and
+    restores both."""
+
+    __slots__ = ("device", "stream", "guard", "outer")
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.guard = self.outer = None
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        if self.stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if self.stream.device != self.device:
+            if self.guard is not None:
+                self.guard.__exit__(None, None, None)
+            raise ValueError(f"stream of {self.stream.device} for tensors on {self.device}")
+        self.outer = torch.cuda.stream(self.stream)
+        self.outer.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.outer is not None:
+            self.outer.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _need_on(t: torch.Tensor, dtype, shape, device, name) -> int:
+    """Data pointer of a contiguous tensor of this type and shape on this device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _need_ws(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if ws is None:
+        return workspace(nbytes, device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: must be a contiguous uint8 tensor on {device}")
+    return ws
+
+
+def _cuda_device(device) -> torch.device:
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("device: must be a CUDA device")
+    return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+
+
+class AdapterPool:
+    """The adapters of one linear as rows of two matrices (the lora_pool_t):
+    A (rows x k) and Bt (rows x d, B transposed), bf16.  Adapter a of rank r
+    has rows first[a] .. first[a] + r; the rows up to the next multiple of 16
+    stay zero.  ``load`` writes an adapter's factors, ``rows_of`` gives its
+    slice, for the factors and for the gradients of lora_requests_bwd."""
+
+    def __init__(self, k: int, d: int, ranks, alphas, device=None):
+        ranks = [int(r) for r in ranks]
+        alphas = [float(a) for a in alphas]
+        if not ranks or len(alphas) != len(ranks):
+            raise ValueError("one rank and one alpha per adapter, at least one adapter")
+        if min(ranks) < 1 or max(ranks) > 256:
+            raise ValueError("ranks must lie in 1..256")
+        if not all(0.0 < a < float("inf") for a in alphas):
+            raise ValueError("alphas must be positive and finite")
+        if k < 8 or d < 8 or k % 8 or d % 8:
+            raise ValueError("k and d must be positive multiples of 8")
+        device = _cuda_device(device)
+        self.k, self.d, self.n, self.device = int(k), int(d), len(ranks), device
+        self.ranks, self.firsts = ranks, []
+        rows = 0
+        for r in ranks:
+            self.firsts.append(rows)
+            rows += (r + 15) // 16 * 16
+        self.rows, self.width = rows, (max(ranks) + 15) // 16 * 16
+        self.A = torch.zeros(rows, k, dtype=torch.bfloat16, device=device)
+        self.Bt = torch.zeros(rows, d, dtype=torch.bfloat16, device=device)
+        self.first = torch.tensor(self.firsts, dtype=torch.int32, device=device)
+        self.rank = torch.tensor(ranks, dtype=torch.int32, device=device)
+        self.scale = torch.tensor([a / r for a, r in zip(alphas, ranks)], dtype=torch.float32, device=device)
+        self._c = _Pool(self.A.data_ptr(), self.Bt.data_ptr(), self.first.data_ptr(), self.rank.data_ptr(),
+                        self.scale.data_ptr(), rows, k, d, self.n, self.width)
+
+    @property
+    def cstruct(self) -> _Pool:
+        return self._c
+
+    def rows_of(self, a: int) -> slice:
+        if not 0 <= a < self.n:
+            raise IndexError(f"adapter {a} of {self.n}")
+        return slice(self.firsts[a], self.firsts[a] + self.ranks[a])
+
+    def load(self, a: int, A: torch.Tensor, B: torch.Tensor) -> None:
+        """Adapter a's factors as the layer holds them: A (r x k), B (d x r)."""
+        rows, r = self.rows_of(a), self.ranks[a]
+        for t, shape, name in ((A, (r, self.k), "A"), (B, (self.d, r), "B")):
+            if t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected bf16 {shape}, got {t.dtype} {tuple(t.shape)}")
+        self.A[rows].copy_(A)
+        self.Bt[rows].copy_(B.t())
+
+
+class RequestPlan:
+    """Device buffers of a batch's maps (the lora_requests_t): n_req requests
+    over T rows and pools of n adapters; see lora_requests_plan."""
+
+    def __init__(self, n_req: int, n: int, T: int, device=None):
+        if n_req < 0 or n < 1 or T < 0:
+            raise ValueError("n_req >= 0, n >= 1 and T >= 0")
+        tiles = lib().lora_requests_max_tiles(n_req, n, T)
+        if tiles <= 0:
+            raise ValueError("at most 4096 requests, 4096 adapters and 2^22 rows")
+        device = _cuda_device(device)
+        self.n_req, self.n, self.T, self.device = int(n_req), int(n), int(T), device
+
+        def ints(count):
+            return torch.zeros(max(count, 4), dtype=torch.int32, device=device)[:count]
+
+        self.starts, self.idx, self.order = ints(n_req + 1), ints(T), ints(T)
+        self.seg, self._tile_first, self._tiles = ints(n + 2), ints(n + 2), ints(4 * tiles)
+        self._c = _Requests(*(t.data_ptr() or self._tiles.data_ptr()
+                              for t in (self.starts, self.idx, self.order, self.seg, self._tile_first, self._tiles)),
+                            T, n_req, n)
+
+    @property
+    def cstruct(self) -> _Requests:
+        return self._c
+
+
+def lora_requests_plan(lens: torch.Tensor, adapters: torch.Tensor, plan: RequestPlan, stream=None) -> RequestPlan:
+    """Fill the plan's maps from the requests' lengths and adapters (int32, device)."""
+    lp = _need_on(lens, torch.int32, (plan.n_req,), plan.device, "lens")
+    ap = _need_on(adapters, torch.int32, (plan.n_req,), plan.device, "adapters")
+    with _On(plan.device, stream) as st:
+        _check(lib().lora_requests_plan(lp or plan._tiles.data_ptr(), ap or plan._tiles.data_ptr(),
+                                        ctypes.byref(plan.cstruct), st), "lora_requests_plan")
+    return plan
+
+
+def _need_match(pool: AdapterPool, plan: RequestPlan):
+    if plan.n != pool.n:
+        raise ValueError(f"plan for {plan.n} adapters, pool of {pool.n}")
+    if plan.device != pool.device:
+        raise ValueError(f"plan on {plan.device}, pool on {pool.device}")
+
+
+def lora_requests_fwd_workspace_bytes(pool: AdapterPool, plan: RequestPlan) -> int:
+    return lib().lora_requests_fwd_workspace_bytes(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct))
+
+
+def lora_requests_bwd_workspace_bytes(pool: AdapterPool, plan: RequestPlan) -> int:
+    return lib().lora_requests_bwd_workspace_bytes(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct))
+
+
+def lora_requests_fwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, base: Optional[torch.Tensor] = None,
+                      Y: Optional[torch.Tensor] = None, U_save: Optional[torch.Tensor] = None,
+                      save: bool = False, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Y = base + each token's adapter term; with ``save`` (or U_save given)
+    also U (T x pool.width, fp32) for the backward.  Y may be ``base``."""
+    _need_match(pool, plan)
+    dev, T, bf = pool.device, plan.T, torch.bfloat16
+    xp = _need_on(X, bf, (T, pool.k), dev, "X")
+    bp = None if base is None else _need_on(base, bf, (T, pool.d), dev, "base")
+    with _On(dev, stream) as st:
+        # rows behind the last request are not written: new outputs start at zero
+        Y = torch.zeros(T, pool.d, dtype=bf, device=dev) if Y is None else Y
+        if U_save is None and save:
+            U_save = torch.zeros(T, pool.width, dtype=torch.float32, device=dev)
+        yp = _need_on(Y, bf, (T, pool.d), dev, "Y")
+        up = None if U_save is None else _need_on(U_save, torch.float32, (T, pool.width), dev, "U_save")
+        if ws is None:
+            ws = workspace(lora_requests_fwd_workspace_bytes(pool, plan), dev)
+        ws = _need_ws(ws, 0, dev)
+        _check(lib().lora_requests_fwd(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct), xp, bp, yp, up,
+                                       ws.data_ptr(), ws.numel(), st), "lora_requests_fwd")
+    return Y, U_save
+
+
+def lora_requests_bwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, U_saved: torch.Tensor, dY: torch.Tensor,
+                      base: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None,
+                      dA: Optional[torch.Tensor] = None, dBt: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None):
+    """dX = base + the adapters' part, and the gradients of the pool's rows dA
+    (rows x k) and dBt (rows x d), fp32."""
+    _need_match(pool, plan)
+    dev, T, bf, f32 = pool.device, plan.T, torch.bfloat16, torch.float32
+    xp = _need_on(X, bf, (T, pool.k), dev, "X")
+    up = _need_on(U_saved, f32, (T, pool.width), dev, "U_saved")
+    gp = _need_on(dY, bf, (T, pool.d), dev, "dY")
+    bp = None if base is None else _need_on(base, bf, (T, pool.k), dev, "base")
+    with _On(dev, stream) as st:
+        dX = torch.zeros(T, pool.k, dtype=bf, device=dev) if dX is None else dX
+        dA = torch.empty(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
+        dBt = torch.empty(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
+        dxp = _need_on(dX, bf, (T, pool.k), dev, "dX")
+        dap = _need_on(dA, f32, (pool.rows, pool.k), dev, "dA")
+        dbp = _need_on(dBt, f32, (pool.rows, pool.d), dev, "dBt")
+        if ws is None:
+            ws = workspace(lora_requests_bwd_workspace_bytes(pool, plan), dev)
+        ws = _need_ws(ws, 0, dev)
+        _check(lib().lora_requests_bwd(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct), xp, up, gp, bp, dxp, dap,
+                                       dbp, ws.data_ptr(), ws.numel(), st), "lora_requests_bwd")
+    return dX, dA, dBt
+
+
+def lora_muon_workspace_bytes(n: int, rows: int, cols: int) -> int:
+    return lib().lora_muon_workspace_bytes(n, rows, cols)
+
+
+def lora_muon_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Tensor, grad: torch.Tensor, lr: float,
+                   momentum: float = 0.95, nesterov: bool = True, scale: float = 1.0, weight_decay: float = 0.0,
+                   eps: float = 1e-7, steps: int = 5, coefs=None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """One step that orthogonalises the momentum of each matrix of a stack
+    (n x rows x cols, or one rows x cols), in place on (master, m) and the
+    bf16 copy; see qlora.h."""
+    if master.dim() not in (2, 3):
+        raise ValueError("master: expected rows x cols or n x rows x cols")
+    n = 1 if master.dim() == 2 else master.shape[0]
+    rows, cols = master.shape[-2], master.shape[-1]
+    dev = master.device
+    if dev.type != "cuda":
+        raise ValueError("master: must be a CUDA tensor")
+    ptrs = [_need_on(t, dt, master.shape, dev, name)
+            for t, dt, name in ((master, torch.float32, "master"), (weight_bf16, torch.bfloat16, "weight_bf16"),
+                                (m, torch.float32, "m"), (grad, torch.float32, "grad"))]
+    cs = None
+    if coefs is not None:
+        if len(coefs) != 3:
+            raise ValueError("coefs: expected three")
+        cs = (ctypes.c_float * 3)(*[float(c) for c in coefs])
+    with _On(dev, stream) as st:
+        if ws is None:
+            ws = workspace(lora_muon_workspace_bytes(n, rows, cols), dev)
+        ws = _need_ws(ws, 0, dev)
+        _check(lib().lora_muon_step(*ptrs, n, rows, cols, float(lr), float(momentum), int(bool(nesterov)), float(scale),
+                                    float(weight_decay), float(eps), int(steps),
+                                    None if cs is None else ctypes.addressof(cs), ws.data_ptr(), ws.numel(), st),
+               "lora_muon_step")
 
 
 def lora_merge(q: NF4Weight, A: torch.Tensor, B: torch.Tensor, alpha: float,

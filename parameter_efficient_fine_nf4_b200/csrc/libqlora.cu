@@ -21,9 +21,11 @@
 #include "adam_kernels.cuh"
 #include "deploy_kernels.cuh"
 #include "gemm_tc.cuh"
+#include "muon_kernels.cuh"
 #include "nf4_gemm.cuh"
 #include "nf4_kernels.cuh"
 #include "ptx.cuh"
+#include "requests_kernels.cuh"
 
 namespace qlora {
 namespace {
@@ -294,6 +296,11 @@ cudaError_t set_deploy_attrs() {
   return fa.maxThreadsPerBlock >= kDeployThreads ? cudaSuccess : cudaErrorLaunchOutOfResources;
 }
 
+cudaError_t set_requests_attrs() {
+  return cudaFuncSetAttribute(requests_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)plan_smem_bytes(kReqMax, kReqMax));
+}
+
 int ensure_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_NO_DEVICE;
@@ -318,7 +325,8 @@ int ensure_device() {
       set_deploy_attrs<true, 2>() != cudaSuccess || set_deploy_attrs<false, 1>() != cudaSuccess ||
       set_deploy_attrs<false, 2>() != cudaSuccess || set_nf4_gemm_attrs<false, false>() != cudaSuccess ||
       set_nf4_gemm_attrs<true, false>() != cudaSuccess || set_nf4_gemm_attrs<false, true>() != cudaSuccess ||
-      set_nf4_gemm_attrs<true, true>() != cudaSuccess || set_small_attrs() != cudaSuccess)
+      set_nf4_gemm_attrs<true, true>() != cudaSuccess || set_small_attrs() != cudaSuccess ||
+      set_requests_attrs() != cudaSuccess)
     return QLORA_ERR_CUDA;
   g_dev_pair_clusters[dev] = pair_clusters_on_device();
   small_cluster_fit(g_dev_cluster_fit[dev]);
@@ -1448,6 +1456,9 @@ const NcclApi& nccl_api() {
   static const NcclApi api = load_nccl();
   return api;
 }
+
+#include "requests_host.inc"
+
 }  // namespace
 
 extern "C" {
@@ -1895,6 +1906,80 @@ int lora_unmerge(const uint16_t* W, const uint16_t* A, const uint16_t* B, int r,
     return QLORA_ERR_UNSUPPORTED_SHAPE;
   return merge_common(nullptr, W, A, B, r, alpha, d, k, W0_out, ws, ws_bytes,
                       reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+// ------------------------------------------------------- many adapters at once
+int64_t lora_requests_max_tiles(int n_req, int n, int64_t T) { return requests_max_tiles(n_req, n, T); }
+
+int lora_requests_plan(const int32_t* lens, const int32_t* adapters, const lora_requests_t* out, qlora_stream_t stream) {
+  QLORA_TRY(check_requests(out));
+  if (!lens || !adapters) return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(ensure_device());
+  return requests_plan(lens, adapters, *out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t lora_requests_fwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req) {
+  if (!pool || !req || check_pool_shape(pool, req) != QLORA_OK) return 0;
+  return carve_requests(nullptr, *pool, *req, false).bytes;
+}
+
+int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X, const uint16_t* base,
+                      uint16_t* Y, float* U_save, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  QLORA_TRY(check_pool(pool, req));
+  if (req->T == 0) return QLORA_OK;
+  if (!X || !Y || !ws) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(base) || !aligned16(Y) || !aligned16(U_save) || !aligned16(ws))
+    return QLORA_ERR_MISALIGNED;
+  const RequestsWs w = carve_requests(ws, *pool, *req, false);
+  if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  QLORA_TRY(ensure_device());
+  return requests_fwd(*pool, *req, X, base, Y, U_save, w, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t lora_requests_bwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req) {
+  if (!pool || !req || check_pool_shape(pool, req) != QLORA_OK) return 0;
+  return carve_requests(nullptr, *pool, *req, true).bytes;
+}
+
+int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X, const float* U_saved,
+                      const uint16_t* dY, const uint16_t* base, uint16_t* dX, float* dA, float* dBt, void* ws,
+                      size_t ws_bytes, qlora_stream_t stream) {
+  QLORA_TRY(check_pool(pool, req));
+  if (!dA || !dBt || !ws) return QLORA_ERR_INVALID_ARG;
+  if (req->T > 0 && (!X || !U_saved || !dY || !dX)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(U_saved) || !aligned16(dY) || !aligned16(base) || !aligned16(dX) || !aligned16(dA) ||
+      !aligned16(dBt) || !aligned16(ws))
+    return QLORA_ERR_MISALIGNED;
+  const RequestsWs w = carve_requests(ws, *pool, *req, true);
+  if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  QLORA_TRY(ensure_device());
+  return requests_bwd(*pool, *req, X, U_saved, dY, base, dX, dA, dBt, w, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t lora_muon_workspace_bytes(int64_t n, int64_t rows, int64_t cols) {
+  if (check_muon_shape(n, rows, cols) != QLORA_OK) return 0;
+  return carve_muon(nullptr, n, rows, cols).bytes;
+}
+
+int lora_muon_step(float* master, uint16_t* weight_bf16, float* m, const float* grad, int64_t n, int64_t rows,
+                   int64_t cols, float lr, float momentum, int nesterov, float scale, float weight_decay, float eps,
+                   int steps, const float* coefs, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  if (!master || !weight_bf16 || !m || !grad || !ws || n < 0) return QLORA_ERR_INVALID_ARG;
+  if (!(lr >= 0.f) || !(momentum >= 0.f && momentum < 1.f) || !std::isfinite(scale) || !(weight_decay >= 0.f) ||
+      !(eps > 0.f) || !std::isfinite(lr) || !std::isfinite(weight_decay) || !std::isfinite(eps) || steps < 1 || steps > 16)
+    return QLORA_ERR_INVALID_ARG;
+  for (int i = 0; coefs && i < 3; ++i)
+    if (!std::isfinite(coefs[i])) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(master) || !aligned16(weight_bf16) || !aligned16(m) || !aligned16(grad) || !aligned16(ws))
+    return QLORA_ERR_MISALIGNED;
+  if (n == 0) return QLORA_OK;
+  QLORA_TRY(check_muon_shape(n, rows, cols));
+  const MuonWs w = carve_muon(ws, n, rows, cols);
+  if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  QLORA_TRY(ensure_device());
+  const float usual[3] = {3.4445f, -4.7750f, 2.0315f};
+  return muon_step(master, weight_bf16, m, grad, n, rows, cols, lr, momentum, nesterov, scale, weight_decay, eps, steps,
+                   coefs ? coefs : usual, w, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int qlora_get_device_status(qlora_stream_t stream, int* status) {
