@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqlora.so")
 SOURCES = ["libqlora.cu"]
 HEADERS = ["ptx.cuh", "nf4_kernels.cuh", "gemm_tc.cuh", "nf4_gemm.cuh", "deploy_kernels.cuh", "adam_kernels.cuh",
-           "requests_kernels.cuh", "requests_host.inc", "muon_kernels.cuh"]
+           "requests_kernels.cuh", "requests_tc.cuh", "requests_host.inc", "muon_kernels.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

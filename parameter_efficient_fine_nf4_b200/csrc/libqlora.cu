@@ -26,6 +26,7 @@
 #include "nf4_kernels.cuh"
 #include "ptx.cuh"
 #include "requests_kernels.cuh"
+#include "requests_tc.cuh"
 
 namespace qlora {
 namespace {
@@ -296,9 +297,14 @@ cudaError_t set_deploy_attrs() {
   return fa.maxThreadsPerBlock >= kDeployThreads ? cudaSuccess : cudaErrorLaunchOutOfResources;
 }
 
+constexpr int kReqSmemMax = 226 * 1024;
 cudaError_t set_requests_attrs() {
-  return cudaFuncSetAttribute(requests_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)plan_smem_bytes(kReqMax, kReqMax));
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(requests_plan_kernel, at, (int)plan_smem_bytes(kReqMax, kReqMax));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_expand_kernel, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel, at, kReqSmemMax);
+  return e;
 }
 
 int ensure_device() {

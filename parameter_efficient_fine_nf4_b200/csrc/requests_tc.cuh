@@ -1,0 +1,682 @@
+// The many-adapter products on tensor cores (tcgen05), for batches of more
+// than a few tokens: tiles of up to 128 tokens of one adapter.
+//
+//   shrink:  V = s X A_a^T        (128 tokens x rank, K columns split over a cluster)
+//   expand:  Y = base + V Bt_a    (128 tokens x a range of columns)
+//   grads:   dA_a = V^T X         (256 columns x rank, tokens split over a cluster)
+// The backward is the same three kernels with A and Bt, X and dY exchanged.
+//
+// V is a 32-bit value kept as three bf16 terms, v = hi + mid + lo (8 bits of
+// significand each), so that products with bf16 factors are exact in fp32:
+// expand multiplies hi and mid (2^-16 of the term, far below the one rounding
+// of its bf16 output), grads all three (its outputs are fp32).  A row of V
+// holds, for each 64 of the adapter's rank (rounded to 16), the columns
+// [hi | mid | lo]; rows are tile by tile, 128 each, and zero behind a tile's
+// tokens.  So V is an ordinary TMA operand for expand (K-major) and for grads
+// (MN-major), with no gather, and only X, dY, base and the outputs are
+// addressed by token.
+//
+// Token rows come in by TMA, 32 at a time where they are consecutive and whole
+// (a request's tokens are) and four at a time (gather4) elsewhere; a gathered
+// row behind the tile's tokens repeats the last one, so nothing that the tile
+// does not own is ever multiplied.
+#pragma once
+#include "ptx.cuh"
+#include "requests_kernels.cuh"
+
+namespace qlora {
+
+constexpr int kReqTile = 128;
+constexpr int kReqThreads = 192;             // warp 0: TMA, warp 1: MMA, warps 2-5: epilogue
+constexpr int kReqRows = 128 * 128;          // bytes of 128 rows x 64 bf16 columns
+
+// Columns of a V row, from the widest adapter of the pool.
+__host__ __device__ __forceinline__ int terms_ld(int width) {
+  return width <= 64 ? (3 * width + 63) / 64 * 64 : (width + 63) / 64 * 192;
+}
+// Column of term `part` of rank index j for an adapter of r16 (rank rounded to 16).
+__device__ __forceinline__ int term_col(int j, int part, int r16) {
+  const int c = j >> 6;
+  const int rc = min(64, r16 - 64 * c);
+  return 192 * c + part * rc + (j & 63);
+}
+
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, const int (&y)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+      : "memory");
+}
+
+// Four consecutive rows of a group of tokens for this lane: rows 4 i .. 4 i + 3
+// of `count`, token numbers from order[first ...]; `whole`: the 32 rows of
+// this lane's group of 8 lanes are all there and consecutive.
+struct RowLane {
+  int tok[4];
+  bool whole;
+};
+__device__ __forceinline__ RowLane row_lane(const int32_t* order, int first, int count, int i) {
+  RowLane r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.tok[j] = order[first + max(0, min(4 * i + j, count - 1))];
+  const int lane = threadIdx.x & 31;
+  const int a = __shfl_sync(0xFFFFFFFFu, r.tok[0], lane & ~7);
+  const int b = __shfl_sync(0xFFFFFFFFu, r.tok[3], lane | 7);
+  r.whole = (i / 8 + 1) * 32 <= count && b - a == 31;
+  return r;
+}
+// This lane's part of one 64-column block of token rows (rounded up to 16).
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row, uint32_t bar, int x,
+                                          const RowLane& r, int i, int count) {
+  if (r.whole) {
+    if (i % 8 == 0) tma_load_2d(dst + (uint32_t)i * 512u, box, bar, x, r.tok[0]);
+  } else if (4 * i < (count + 15) / 16 * 16) {
+    tma_gather4(dst + (uint32_t)i * 512u, row, bar, x, r.tok);
+  }
+}
+__device__ __forceinline__ uint32_t row_bytes(int count) { return (uint32_t)((count + 15) / 16 * 16 * 128); }
+
+__device__ __forceinline__ float bf16_round(float v, uint16_t& bits) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  bits = *reinterpret_cast<const uint16_t*>(&h);
+  return __bfloat162float(h);
+}
+
+// Writes four consecutive rank values (j % 4 == 0) of one V row as three terms.
+__device__ __forceinline__ void store_terms(uint16_t* row, int j, int r16, const float (&v)[4]) {
+  uint16_t t[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float h = bf16_round(v[i], t[0][i]);
+    const float rest = __fsub_rn(v[i], h);
+    const float m = bf16_round(rest, t[1][i]);
+    bf16_round(__fsub_rn(rest, m), t[2][i]);
+  }
+#pragma unroll
+  for (int part = 0; part < 3; ++part)
+    *reinterpret_cast<uint2*>(row + term_col(j, part, r16)) =
+        make_uint2((uint32_t)t[part][0] | ((uint32_t)t[part][1] << 16), (uint32_t)t[part][2] | ((uint32_t)t[part][3] << 16));
+}
+
+// A shared-memory ring of stages with full and empty barriers.
+struct Ring {
+  uint32_t full, empty;          // first barrier of each, 8 bytes apart
+  int stages;
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ uint32_t full_bar() const { return full + 8u * at; }
+  __device__ __forceinline__ uint32_t empty_bar() const { return empty + 8u * at; }
+  __device__ __forceinline__ void next() {
+    if (++at == stages) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// ---------------------------------------------------------------------- shrink
+struct ShrinkArgs {
+  const int32_t* order;
+  const int4* tiles;
+  PoolArgs pool;
+  int K, width, csize, stages, tmem_cols, stage_bytes, ld;
+  float* U;                     // T x width, or null: the unscaled product
+  uint16_t* V;                  // terms of scale * product
+  const float* U_in;            // T x width, or null: a saved U ...
+  uint16_t* V_in;               // ... whose terms (times the scale) are laid out as well
+};
+
+// X is streamed once; the factor's rows come from L2.  HBM-bound at ranks up
+// to 64; the split over the cluster only makes enough CTAs.
+__global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __grid_constant__ CUtensorMap box,
+                                                                      const __grid_constant__ CUtensorMap row,
+                                                                      const __grid_constant__ CUtensorMap weight,
+                                                                      const __grid_constant__ ShrinkArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = (int)(blockIdx.x % p.csize), u = (int)(blockIdx.x / p.csize);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int4 tile = p.tiles[u];
+  if (tile.z <= 0) return;                       // the whole cluster
+  const int count = min(tile.z, kReqTile);
+  const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
+  if (ad.rank == 0) {
+    if (p.U && q == 0)
+      for (int e = threadIdx.x; e < count * p.width; e += kReqThreads)
+        p.U[(int64_t)p.order[tile.y + e / p.width] * p.width + e % p.width] = 0.f;
+    return;
+  }
+  const int r16 = (ad.rank + 15) & ~15;
+  const int kper = ((p.K + p.csize - 1) / p.csize + 63) / 64 * 64;
+  const int k0 = min(p.K, q * kper), k1 = min(p.K, k0 + kper);
+  const int steps = (k1 - k0 + 63) / 64;
+  volatile int* abort_flag = &s_abort;
+
+  Ring ring;
+  ring.full = smem_u32(&s_bar[0]);
+  ring.empty = smem_u32(&s_bar[8]);
+  ring.stages = p.stages;
+  const uint32_t done_bar = smem_u32(&s_bar[16]);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(ring.full + 8u * i, 1);
+      mbar_init(ring.empty + 8u * i, 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), (uint32_t)p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    const RowLane r = row_lane(p.order, tile.y, count, lane);
+    const uint32_t bytes = row_bytes(count) + (uint32_t)r16 * 128u;
+    int issued = 0;
+    for (int s = 0; s < steps; ++s) {
+      int ok = 1;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
+        if (ok) mbar_arrive_expect_tx(ring.full_bar(), bytes);
+      }
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
+      const int x = k0 + s * 64;
+      load_rows(st, &box, &row, ring.full_bar(), x, r, lane, count);
+      if (lane < r16 / 16)
+        tma_load_2d(st + kReqRows + (uint32_t)lane * 2048u, &weight, ring.full_bar(), x, ad.first + 16 * lane);
+      ring.next();
+      ++issued;
+    }
+    if (*abort_flag && lane == 0) {              // let copies in flight land
+      for (int i = 0; i < min(issued, p.stages); ++i) {
+        const int last = (issued - 1 - i) / p.stages;      // last use of stage i counts from 0
+        mbar_wait_bounded(ring.full + 8u * i, (uint32_t)(last & 1), nullptr);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16_f32(128, r16, 0, 0);
+    bool ok = true;
+    int any = 0;
+    for (int s = 0; s < steps && ok; ++s) {
+      ok = mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
+      const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kReqRows, 16, 1024);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_bf16(tmem, a + 2u * j, b + 2u * j, idesc, (s | j) ? 1u : 0u);
+      any = 1;
+      umma_commit(ring.empty_bar());
+      ring.next();
+    }
+    if (any) {
+      umma_commit(done_bar);
+      if (!ok) mbar_wait_bounded(done_bar, 0, nullptr);
+    }
+  }
+  __syncwarp();
+
+  // partial product to shared memory (the stages are free once the MMAs are done)
+  const int pitch = r16 + 4;
+  float* s_part = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int quarter = warp & 3, rowi = quarter * 32 + lane;
+    bool ok = true;
+    if (steps > 0) {
+      ok = mbar_wait_bounded(done_bar, 0, abort_flag);
+      tc_fence_after();
+    }
+    for (int c = 0; c < r16; c += 16) {
+      uint32_t v[16];
+      if (steps > 0 && ok) {
+        tmem_ld_32x32b_x16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(s_part + rowi * pitch + c + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+  if (p.csize > 1) cluster_sync();
+
+  // this CTA's share of the rows: partials added in rank order
+  const int rows = kReqTile / p.csize, w4 = p.width / 4;
+  const uint32_t part = smem_u32(s_part);
+  for (int e = threadIdx.x; e < rows * w4; e += kReqThreads) {
+    const int i = q * rows + e / w4, j = (e % w4) * 4;
+    const bool valid = i < count;
+    const int64_t tok = valid ? p.order[tile.y + i] : 0;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (valid && j < r16) {
+      const uint32_t at = part + (uint32_t)(i * pitch + j) * 4u;
+      for (int c = 0; c < p.csize; ++c) {
+        const float4 f = p.csize > 1 ? ld_shared_cluster_f4(mapa_shared(at, (uint32_t)c))
+                                     : *reinterpret_cast<const float4*>(s_part + i * pitch + j);
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (j + n >= ad.rank) v[n] = 0.f;
+    }
+    if (p.U && valid) *reinterpret_cast<float4*>(p.U + tok * p.width + j) = make_float4(v[0], v[1], v[2], v[3]);
+    if (j < r16) {
+      const int64_t vrow = ((int64_t)u * kReqTile + i) * p.ld;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) v[n] = __fmul_rn(ad.scale, v[n]);
+      store_terms(p.V + vrow, j, r16, v);
+      if (p.V_in) {
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        if (valid) {
+          const float4 f = *reinterpret_cast<const float4*>(p.U_in + tok * p.width + j);
+          w[0] = f.x; w[1] = f.y; w[2] = f.z; w[3] = f.w;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) w[n] = j + n < ad.rank ? __fmul_rn(ad.scale, w[n]) : 0.f;
+        store_terms(p.V_in + vrow, j, r16, w);
+      }
+    }
+  }
+  if (p.csize > 1) cluster_sync();               // partials stay until every CTA has read them
+}
+
+// ---------------------------------------------------------------------- expand
+struct ExpandArgs {
+  const int32_t* order;
+  const int4* tiles;
+  PoolArgs pool;
+  int N, width, range, ranges, stages, stage_bytes, v_bytes;
+  const uint16_t* base;
+  uint16_t* out;
+};
+
+// Streams base in and Y out, 64 columns of the tile's rows a stage, with a few
+// small MMAs (two per 16 of the rank) in between: HBM-bound.
+__global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __grid_constant__ CUtensorMap box,
+                                                                      const __grid_constant__ CUtensorMap row,
+                                                                      const __grid_constant__ CUtensorMap weight,
+                                                                      const __grid_constant__ CUtensorMap terms,
+                                                                      const __grid_constant__ ExpandArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 5];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = (int)(blockIdx.x / p.ranges);
+  const int n0 = (int)(blockIdx.x % p.ranges) * p.range, n1 = min(p.N, n0 + p.range);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int4 tile = p.tiles[u];
+  if (tile.z <= 0) return;
+  const int count = min(tile.z, kReqTile);
+  const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
+  if (ad.rank == 0) {
+    if (p.out != p.base) {
+      const int n8 = (n1 - n0) / 8;
+      for (int e = threadIdx.x; e < count * n8; e += kReqThreads) {
+        const int64_t at = (int64_t)p.order[tile.y + e / n8] * p.N + n0 + (e % n8) * 8;
+        *reinterpret_cast<uint4*>(p.out + at) = p.base ? *reinterpret_cast<const uint4*>(p.base + at) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+  const int r16 = (ad.rank + 15) & ~15;
+  const int chunks = (n1 - n0 + 63) / 64;
+  volatile int* abort_flag = &s_abort;
+
+  Ring ring;
+  ring.full = smem_u32(&s_bar[0]);
+  ring.empty = smem_u32(&s_bar[8]);
+  ring.stages = p.stages;
+  const uint32_t v_bar = smem_u32(&s_bar[16]);
+  const uint32_t acc_full = smem_u32(&s_bar[17]), acc_empty = smem_u32(&s_bar[19]);   // two each
+  const uint32_t stage0 = sbase + (uint32_t)p.v_bytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(ring.full + 8u * i, 1);
+      mbar_init(ring.empty + 8u * i, 4);
+    }
+    mbar_init(v_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8u * i, 1);
+      mbar_init(acc_empty + 8u * i, 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    const RowLane r = row_lane(p.order, tile.y, count, lane);
+    const uint32_t bytes = (p.base ? row_bytes(count) : 0u) + (uint32_t)r16 * 128u;
+    // V: hi and mid of every 64 of the rank, in boxes of 64 columns
+    if (lane == 0) {
+      int boxes = 0;
+      for (int c = 0; c < r16; c += 64) boxes += (2 * min(64, r16 - c) + 63) / 64;
+      mbar_arrive_expect_tx(v_bar, (uint32_t)(boxes * kReqRows));
+      int at = 0;
+      for (int c = 0; c < r16; c += 64)
+        for (int i = 0; i < (2 * min(64, r16 - c) + 63) / 64; ++i, ++at)
+          tma_load_2d(sbase + (uint32_t)(at * kReqRows), &terms, v_bar, c * 3 + 64 * i, u * kReqTile);
+    }
+    int issued = 0;
+    for (int s = 0; s < chunks; ++s) {
+      int ok = 1;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
+        if (ok) mbar_arrive_expect_tx(ring.full_bar(), bytes);
+      }
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      const uint32_t st = stage0 + (uint32_t)(ring.at * p.stage_bytes);
+      const int x = n0 + s * 64;
+      if (p.base) load_rows(st, &box, &row, ring.full_bar(), x, r, lane, count);
+      if (lane < r16 / 16)
+        tma_load_2d(st + kReqRows + (uint32_t)lane * 2048u, &weight, ring.full_bar(), x, ad.first + 16 * lane);
+      ring.next();
+      ++issued;
+    }
+    if (*abort_flag && lane == 0) {
+      mbar_wait_bounded(v_bar, 0, nullptr);
+      for (int i = 0; i < min(issued, p.stages); ++i) {
+        const int last = (issued - 1 - i) / p.stages;
+        mbar_wait_bounded(ring.full + 8u * i, (uint32_t)(last & 1), nullptr);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16_f32(128, 64, 0, 1);
+    bool ok = mbar_wait_bounded(v_bar, 0, abort_flag);
+    int any = 0, last = 0;
+    for (int s = 0; s < chunks && ok; ++s) {
+      const int buf = s & 1;
+      ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((s >> 1) & 1) ^ 1), abort_flag) &&
+           mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(buf * 64);
+      const uint32_t w = stage0 + (uint32_t)(ring.at * p.stage_bytes) + kReqRows;
+      uint32_t acc = 0;
+      for (int c = 0; c < r16; c += 64) {
+        const int rc = min(64, r16 - c);
+        const uint32_t vb = sbase + (uint32_t)(c / 64 * 2 * kReqRows);
+        for (int k = 0; k < 2 * rc; k += 16) {          // hi, then mid
+          const int wr = c + (k < rc ? k : k - rc);
+          const uint64_t a = smem_desc_sw128(vb + (uint32_t)(k / 64 * kReqRows + (k & 63) * 2), 16, 1024);
+          const uint64_t b = smem_desc_sw128(w + (uint32_t)wr * 128u, 8192, 1024);
+          umma_bf16(d, a, b, idesc, acc);
+          acc = 1;
+        }
+      }
+      any = 1;
+      last = buf;
+      umma_commit(acc_full + 8u * buf);
+      ring.next();
+    }
+    if (!ok && any) mbar_wait_bounded(acc_full + 8u * last, 0, nullptr);
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, rowi = quarter * 32 + lane;
+    const int tok = p.order[tile.y + min(rowi, count - 1)];
+    for (int s = 0; s < chunks; ++s) {
+      const int buf = s & 1;
+      bool ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag) &&
+                mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      uint32_t v[64];
+      {
+        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
+        const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 64);
+        tmem_ld_32x32b_x32(t, lo);
+        tmem_ld_32x32b_x32(t + 32, hi);
+        tmem_ld_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
+      // base + term, in place in the stage (128B-swizzled rows: conflict-free)
+      uint8_t* st = smem + p.v_bytes + ring.at * p.stage_bytes;
+      uint8_t* mine = st + rowi * 128;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(mine + ((c ^ (rowi & 7)) << 4));
+        uint4 b = p.base ? *at : make_uint4(0, 0, 0, 0);
+        uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(w[j]) + __uint_as_float(v[8 * c + 2 * j]),
+                                                         bf_hi(w[j]) + __uint_as_float(v[8 * c + 2 * j + 1]));
+          w[j] = *reinterpret_cast<const uint32_t*>(&o);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      const int x = n0 + s * 64 + (lane & 7) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = quarter * 32 + i * 4 + lane / 8;
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, tok, i * 4 + lane / 8);
+        if (r < count && x < n1)
+          *reinterpret_cast<uint4*>(p.out + t * p.N + x) =
+              *reinterpret_cast<const uint4*>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+      }
+      fence_proxy_async_smem();                  // the next copy into this stage comes by TMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ring.empty_bar());
+      ring.next();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 128);
+}
+
+// ----------------------------------------------------------------------- grads
+struct GradArgs {
+  const int32_t* order;
+  const int32_t* seg;
+  const int32_t* tile_first;
+  PoolArgs pool;
+  int cols[2], blocks[2];       // columns of the two factors, and their blocks of 256
+  float* dW[2];
+  int width, chunks, csize, stages, stage_bytes, tmem_cols;
+};
+constexpr int kGradCols = 256;
+
+// One adapter, 64 of its rank, 256 columns: D[column][hi | mid | lo] sums over
+// the adapter's tokens (A operand: token rows, MN-major; B operand: V,
+// MN-major), the CTAs of a cluster taking every csize-th 64 tokens; the three
+// parts and the CTAs' sums are added in a fixed order.
+__global__ void __launch_bounds__(kReqThreads) requests_grads_kernel(
+    const __grid_constant__ CUtensorMap box0, const __grid_constant__ CUtensorMap row0, const __grid_constant__ CUtensorMap terms0,
+    const __grid_constant__ CUtensorMap box1, const __grid_constant__ CUtensorMap row1, const __grid_constant__ CUtensorMap terms1,
+    const __grid_constant__ GradArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = (int)(blockIdx.x % p.csize);
+  int unit = (int)(blockIdx.x / p.csize);
+  const int per = p.blocks[0] + p.blocks[1];
+  const int block = unit % per;
+  unit /= per;
+  const int rc0 = (unit % p.chunks) * 64;
+  const int a = unit / p.chunks;
+  const int z = block >= p.blocks[0] ? 1 : 0;
+  const int cols = z ? p.cols[1] : p.cols[0];
+  const int c0 = (z ? block - p.blocks[0] : block) * kGradCols;
+  griddep_wait();
+  griddep_launch_dependents();
+  const AdapterRows ad = adapter_rows(p.pool, a, p.width);
+  if (rc0 >= ad.rank) return;                    // the whole cluster
+  const int rc = min(64, ((ad.rank + 15) & ~15) - rc0);
+  const int lo = p.seg[a], cnt = p.seg[a + 1] - lo;
+  const int vrow0 = p.tile_first[a] * kReqTile;
+  const int all = (cnt + 63) / 64;
+  const int steps = all > q ? (all - q + p.csize - 1) / p.csize : 0;
+  const CUtensorMap* box = z ? &box1 : &box0;
+  const CUtensorMap* rowm = z ? &row1 : &row0;
+  const CUtensorMap* terms = z ? &terms1 : &terms0;
+  float* dW = z ? p.dW[1] : p.dW[0];
+  const int halves = cols - c0 > 128 ? 2 : 1;    // 128-column MMAs in use
+  const int blocks64 = min(4, (cols - c0 + 63) / 64);   // (an unloaded last block is never stored)
+  const int vboxes = (3 * rc + 63) / 64;
+  volatile int* abort_flag = &s_abort;
+
+  Ring ring;
+  ring.full = smem_u32(&s_bar[0]);
+  ring.empty = smem_u32(&s_bar[8]);
+  ring.stages = p.stages;
+  const uint32_t done_bar = smem_u32(&s_bar[16]);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(ring.full + 8u * i, 1);
+      mbar_init(ring.empty + 8u * i, 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), (uint32_t)p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    const int i = lane & 15;                     // four token rows of 64
+    int issued = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int first = (q + s * p.csize) * 64;
+      const int m = min(64, cnt - first);
+      const RowLane r = row_lane(p.order, lo + first, m, i);
+      int ok = 1;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
+        if (ok) mbar_arrive_expect_tx(ring.full_bar(), row_bytes(m) * blocks64 + (uint32_t)vboxes * 8192u);
+      }
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
+      for (int c = lane >> 4; c < blocks64; c += 2)
+        load_rows(st + (uint32_t)c * 8192u, box, rowm, ring.full_bar(), c0 + c * 64, r, i, m);
+      if (lane < vboxes)
+        tma_load_2d(st + 4u * 8192u + (uint32_t)lane * 8192u, terms, ring.full_bar(), rc0 * 3 + 64 * lane, vrow0 + first);
+      ring.next();
+      ++issued;
+    }
+    if (*abort_flag && lane == 0) {
+      for (int k = 0; k < min(issued, p.stages); ++k) {
+        const int last = (issued - 1 - k) / p.stages;
+        mbar_wait_bounded(ring.full + 8u * k, (uint32_t)(last & 1), nullptr);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16_f32(128, 3 * rc, 1, 1);
+    bool ok = true;
+    int any = 0;
+    for (int s = 0; s < steps && ok; ++s) {
+      ok = mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int m = min(64, cnt - (q + s * p.csize) * 64);
+      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
+      for (int h = 0; h < halves; ++h)
+        for (int k = 0; k < (m + 15) / 16; ++k)
+          umma_bf16(tmem + (uint32_t)(h * 3 * rc), smem_desc_sw128(st + (uint32_t)(h * 16384 + k * 2048), 8192, 1024),
+                    smem_desc_sw128(st + 4u * 8192u + (uint32_t)k * 2048u, 8192, 1024), idesc, (s | k) ? 1u : 0u);
+      any = 1;
+      umma_commit(ring.empty_bar());
+      ring.next();
+    }
+    if (any) {
+      umma_commit(done_bar);
+      if (!ok) mbar_wait_bounded(done_bar, 0, nullptr);
+    }
+  }
+  __syncwarp();
+
+  // [rank][column] sums of this CTA in shared memory
+  float* s_part = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int quarter = warp & 3;
+    bool ok = true;
+    if (steps > 0) {
+      ok = mbar_wait_bounded(done_bar, 0, abort_flag);
+      tc_fence_after();
+    }
+    for (int h = 0; h < halves; ++h)
+      for (int j = 0; j < rc; j += 16) {
+        uint32_t v[3][16];
+        if (steps > 0 && ok) {
+          const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(h * 3 * rc + j);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) tmem_ld_32x32b_x16(t + (uint32_t)(part * rc), v[part]);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[part][i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s_part[(j + i) * kGradCols + h * 128 + quarter * 32 + lane] =
+              __uint_as_float(v[0][i]) + (__uint_as_float(v[1][i]) + __uint_as_float(v[2][i]));
+      }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+  if (p.csize > 1) cluster_sync();
+  const uint32_t part = smem_u32(s_part);
+  const int per_cta = (rc * (kGradCols / 4) + p.csize - 1) / p.csize;
+  const int e1 = min(rc * (kGradCols / 4), (q + 1) * per_cta);
+  for (int e = q * per_cta + threadIdx.x; e < e1; e += kReqThreads) {
+    const int j = e / (kGradCols / 4), c = (e % (kGradCols / 4)) * 4;
+    if (c0 + c >= cols) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t at = part + (uint32_t)(j * kGradCols + c) * 4u;
+    for (int k = 0; k < p.csize; ++k) {
+      const float4 f = p.csize > 1 ? ld_shared_cluster_f4(mapa_shared(at, (uint32_t)k))
+                                   : *reinterpret_cast<const float4*>(s_part + j * kGradCols + c);
+      v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+    }
+    *reinterpret_cast<float4*>(dW + (int64_t)(ad.first + rc0 + j) * cols + c0 + c) = v;
+  }
+  if (p.csize > 1) cluster_sync();
+}
+
+}  // namespace qlora
