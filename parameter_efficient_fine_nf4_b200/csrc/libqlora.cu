@@ -301,9 +301,12 @@ constexpr int kReqSmemMax = 226 * 1024;
 cudaError_t set_requests_attrs() {
   const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(requests_plan_kernel, at, (int)plan_smem_bytes(kReqMax, kReqMax));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<2>, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<4>, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<8>, at, kReqSmemMax);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_expand_kernel, at, kReqSmemMax);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel<1>, at, kReqSmemMax);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel<4>, at, kReqSmemMax);
   return e;
 }
 

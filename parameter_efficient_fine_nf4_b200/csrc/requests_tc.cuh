@@ -10,8 +10,8 @@
 // significand each), so that products with bf16 factors are exact in fp32:
 // expand multiplies hi and mid (2^-16 of the term, far below the one rounding
 // of its bf16 output), grads all three (its outputs are fp32).  A row of V
-// holds, for each 64 of the adapter's rank (rounded to 16), the columns
-// [hi | mid | lo]; rows are tile by tile, 128 each, and zero behind a tile's
+// holds, for each 64 of the adapter's rank (rounded to 16), 64 columns for hi,
+// then mid | lo side by side.  Rows are tile by tile, 128 each, and zero behind a tile's
 // tokens.  So V is an ordinary TMA operand for expand (K-major) and for grads
 // (MN-major), with no gather, and only X, dY, base and the outputs are
 // addressed by token.
@@ -20,6 +20,12 @@
 // (a request's tokens are) and four at a time (gather4) elsewhere; a gathered
 // row behind the tile's tokens repeats the last one, so nothing that the tile
 // does not own is ever multiplied.
+//
+// The tensor core adds into its 32-bit accumulator by cutting, not rounding:
+// measured, a sum over 5,500 tokens in one accumulator is 7e-5 off, always
+// towards zero.  So an accumulator whose result is kept in 32 bits takes one
+// stage (64 of the long sum) only; two alternate, and the epilogue warps add
+// each to registers, rounding to nearest, while the other one fills.
 #pragma once
 #include "ptx.cuh"
 #include "requests_kernels.cuh"
@@ -28,17 +34,18 @@ namespace qlora {
 
 constexpr int kReqTile = 128;
 constexpr int kReqThreads = 192;             // warp 0: TMA, warp 1: MMA, warps 2-5: epilogue
+constexpr int kShrinkThreads = 320;          // warps 2-9: epilogue, two per quarter of the rows
 constexpr int kReqRows = 128 * 128;          // bytes of 128 rows x 64 bf16 columns
 
 // Columns of a V row, from the widest adapter of the pool.
 __host__ __device__ __forceinline__ int terms_ld(int width) {
-  return width <= 64 ? (3 * width + 63) / 64 * 64 : (width + 63) / 64 * 192;
+  return width <= 64 ? 64 + (2 * width + 63) / 64 * 64 : (width + 63) / 64 * 192;
 }
 // Column of term `part` of rank index j for an adapter of r16 (rank rounded to 16).
 __device__ __forceinline__ int term_col(int j, int part, int r16) {
   const int c = j >> 6;
   const int rc = min(64, r16 - 64 * c);
-  return 192 * c + part * rc + (j & 63);
+  return 192 * c + (part == 0 ? 0 : 64 + (part - 1) * rc) + (j & 63);
 }
 
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, const int (&y)[4]) {
@@ -128,13 +135,15 @@ struct ShrinkArgs {
 };
 
 // X is streamed once; the factor's rows come from L2.  HBM-bound at ranks up
-// to 64; the split over the cluster only makes enough CTAs.
-__global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __grid_constant__ CUtensorMap box,
+// to 64; the split over the cluster only makes enough CTAs.  NI: 32 columns of
+// the rank per step of the epilogue's registers (width <= 32 NI).
+template <int NI>
+__global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const __grid_constant__ CUtensorMap box,
                                                                       const __grid_constant__ CUtensorMap row,
                                                                       const __grid_constant__ CUtensorMap weight,
                                                                       const __grid_constant__ ShrinkArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 2];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -149,7 +158,7 @@ __global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __gr
   const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
   if (ad.rank == 0) {
     if (p.U && q == 0)
-      for (int e = threadIdx.x; e < count * p.width; e += kReqThreads)
+      for (int e = threadIdx.x; e < count * p.width; e += kShrinkThreads)
         p.U[(int64_t)p.order[tile.y + e / p.width] * p.width + e % p.width] = 0.f;
     return;
   }
@@ -163,13 +172,16 @@ __global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __gr
   ring.full = smem_u32(&s_bar[0]);
   ring.empty = smem_u32(&s_bar[8]);
   ring.stages = p.stages;
-  const uint32_t done_bar = smem_u32(&s_bar[16]);
+  const uint32_t acc_full = smem_u32(&s_bar[16]), acc_empty = smem_u32(&s_bar[18]);   // two each
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(ring.full + 8u * i, 1);
       mbar_init(ring.empty + 8u * i, 1);
     }
-    mbar_init(done_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8u * i, 1);
+      mbar_init(acc_empty + 8u * i, 8);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -210,50 +222,68 @@ __global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __gr
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_bf16_f32(128, r16, 0, 0);
     bool ok = true;
-    int any = 0;
+    int last = -1;
     for (int s = 0; s < steps && ok; ++s) {
-      ok = mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      const int buf = s & 1;
+      ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((s >> 1) & 1) ^ 1), abort_flag) &&
+           mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
       const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kReqRows, 16, 1024);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) umma_bf16(tmem, a + 2u * j, b + 2u * j, idesc, (s | j) ? 1u : 0u);
-      any = 1;
+      for (int j = 0; j < 4; ++j) umma_bf16(tmem + (uint32_t)(buf * r16), a + 2u * j, b + 2u * j, idesc, j ? 1u : 0u);
+      last = s;
       umma_commit(ring.empty_bar());
+      umma_commit(acc_full + 8u * buf);
       ring.next();
     }
-    if (any) {
-      umma_commit(done_bar);
-      if (!ok) mbar_wait_bounded(done_bar, 0, nullptr);
-    }
+    if (!ok && last >= 0) mbar_wait_bounded(acc_full + 8u * (last & 1), (uint32_t)((last >> 1) & 1), nullptr);
   }
   __syncwarp();
 
-  // partial product to shared memory (the stages are free once the MMAs are done)
+  // the stages' products added up in registers, then to shared memory (all
+  // stages are free once the last MMA is done)
   const int pitch = r16 + 4;
   float* s_part = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
-    const int quarter = warp & 3, rowi = quarter * 32 + lane;
-    bool ok = true;
-    if (steps > 0) {
-      ok = mbar_wait_bounded(done_bar, 0, abort_flag);
+    const int quarter = warp & 3, half = (warp - 2) >> 2, rowi = quarter * 32 + lane;
+    float acc[NI][16];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+    for (int s = 0; s < steps; ++s) {
+      const int buf = s & 1;
+      if (!mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag)) break;
+      __syncwarp();
       tc_fence_after();
-    }
-    for (int c = 0; c < r16; c += 16) {
-      uint32_t v[16];
-      if (steps > 0 && ok) {
-        tmem_ld_32x32b_x16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
-        tmem_ld_wait();
-      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0u;
+      for (int i = 0; i < NI; ++i) {
+        const int c = 32 * i + 16 * half;
+        if (c < r16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * r16 + c), v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[j]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(s_part + rowi * pitch + c + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
     }
-    tc_fence_before();
+    // the partial sums lie over the stages: every epilogue warp has seen the last product
+    named_bar_sync(1, 256);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int c = 32 * i + 16 * half;
+      if (c < r16)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<float4*>(s_part + rowi * pitch + c + 4 * j) =
+              make_float4(acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]);
+    }
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
@@ -262,7 +292,7 @@ __global__ void __launch_bounds__(kReqThreads) requests_shrink_kernel(const __gr
   // this CTA's share of the rows: partials added in rank order
   const int rows = kReqTile / p.csize, w4 = p.width / 4;
   const uint32_t part = smem_u32(s_part);
-  for (int e = threadIdx.x; e < rows * w4; e += kReqThreads) {
+  for (int e = threadIdx.x; e < rows * w4; e += kShrinkThreads) {
     const int i = q * rows + e / w4, j = (e % w4) * 4;
     const bool valid = i < count;
     const int64_t tok = valid ? p.order[tile.y + i] : 0;
@@ -379,13 +409,10 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
     const uint32_t bytes = (p.base ? row_bytes(count) : 0u) + (uint32_t)r16 * 128u;
     // V: hi and mid of every 64 of the rank, in boxes of 64 columns
     if (lane == 0) {
-      int boxes = 0;
-      for (int c = 0; c < r16; c += 64) boxes += (2 * min(64, r16 - c) + 63) / 64;
+      const int boxes = 2 * ((r16 + 63) / 64);
       mbar_arrive_expect_tx(v_bar, (uint32_t)(boxes * kReqRows));
-      int at = 0;
-      for (int c = 0; c < r16; c += 64)
-        for (int i = 0; i < (2 * min(64, r16 - c) + 63) / 64; ++i, ++at)
-          tma_load_2d(sbase + (uint32_t)(at * kReqRows), &terms, v_bar, c * 3 + 64 * i, u * kReqTile);
+      for (int i = 0; i < boxes; ++i)
+        tma_load_2d(sbase + (uint32_t)(i * kReqRows), &terms, v_bar, (i >> 1) * 192 + (i & 1) * 64, u * kReqTile);
     }
     int issued = 0;
     for (int s = 0; s < chunks; ++s) {
@@ -427,8 +454,8 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
         const int rc = min(64, r16 - c);
         const uint32_t vb = sbase + (uint32_t)(c / 64 * 2 * kReqRows);
         for (int k = 0; k < 2 * rc; k += 16) {          // hi, then mid
-          const int wr = c + (k < rc ? k : k - rc);
-          const uint64_t a = smem_desc_sw128(vb + (uint32_t)(k / 64 * kReqRows + (k & 63) * 2), 16, 1024);
+          const int kk = k < rc ? k : k - rc, wr = c + kk;
+          const uint64_t a = smem_desc_sw128(vb + (uint32_t)((k < rc ? 0 : kReqRows) + kk * 2), 16, 1024);
           const uint64_t b = smem_desc_sw128(w + (uint32_t)wr * 128u, 8192, 1024);
           umma_bf16(d, a, b, idesc, acc);
           acc = 1;
@@ -513,13 +540,16 @@ constexpr int kGradCols = 256;
 // One adapter, 64 of its rank, 256 columns: D[column][hi | mid | lo] sums over
 // the adapter's tokens (A operand: token rows, MN-major; B operand: V,
 // MN-major), the CTAs of a cluster taking every csize-th 64 tokens; the three
-// parts and the CTAs' sums are added in a fixed order.
-__global__ void __launch_bounds__(kReqThreads) requests_grads_kernel(
+// parts and the CTAs' sums are added in a fixed order.  Only the hi part is
+// moved to registers stage by stage: mid and lo are 2^-8 of it and may be cut
+// 2^8 times as often.
+template <int NI>                                // 16 of the rank each: 1 or 4
+__global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_kernel(
     const __grid_constant__ CUtensorMap box0, const __grid_constant__ CUtensorMap row0, const __grid_constant__ CUtensorMap terms0,
     const __grid_constant__ CUtensorMap box1, const __grid_constant__ CUtensorMap row1, const __grid_constant__ CUtensorMap terms1,
     const __grid_constant__ GradArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 2];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -550,20 +580,25 @@ __global__ void __launch_bounds__(kReqThreads) requests_grads_kernel(
   float* dW = z ? p.dW[1] : p.dW[0];
   const int halves = cols - c0 > 128 ? 2 : 1;    // 128-column MMAs in use
   const int blocks64 = min(4, (cols - c0 + 63) / 64);   // (an unloaded last block is never stored)
-  const int vboxes = (3 * rc + 63) / 64;
+  const int vboxes = 1 + (2 * rc + 63) / 64;
   volatile int* abort_flag = &s_abort;
 
   Ring ring;
   ring.full = smem_u32(&s_bar[0]);
   ring.empty = smem_u32(&s_bar[8]);
   ring.stages = p.stages;
-  const uint32_t done_bar = smem_u32(&s_bar[16]);
+  const uint32_t acc_full = smem_u32(&s_bar[16]), acc_empty = smem_u32(&s_bar[18]);   // two each
+  // Tensor Memory: hi of each half in two alternating sets, then mid | lo of each half
+  const uint32_t rcw = (uint32_t)min(64, p.width);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(ring.full + 8u * i, 1);
       mbar_init(ring.empty + 8u * i, 1);
     }
-    mbar_init(done_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8u * i, 1);
+      mbar_init(acc_empty + 8u * i, 4);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -604,27 +639,32 @@ __global__ void __launch_bounds__(kReqThreads) requests_grads_kernel(
       }
     }
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16_f32(128, 3 * rc, 1, 1);
+    const uint32_t id_hi = idesc_bf16_f32(128, rc, 1, 1), id_rest = idesc_bf16_f32(128, 2 * rc, 1, 1);
     bool ok = true;
-    int any = 0;
+    int last = -1;
     for (int s = 0; s < steps && ok; ++s) {
-      ok = mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+      const int buf = s & 1;
+      ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((s >> 1) & 1) ^ 1), abort_flag) &&
+           mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
       if (!ok) break;
       tc_fence_after();
       const int m = min(64, cnt - (q + s * p.csize) * 64);
       const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
-      for (int h = 0; h < halves; ++h)
-        for (int k = 0; k < (m + 15) / 16; ++k)
-          umma_bf16(tmem + (uint32_t)(h * 3 * rc), smem_desc_sw128(st + (uint32_t)(h * 16384 + k * 2048), 8192, 1024),
-                    smem_desc_sw128(st + 4u * 8192u + (uint32_t)k * 2048u, 8192, 1024), idesc, (s | k) ? 1u : 0u);
-      any = 1;
+      const uint32_t v = st + 4u * 8192u;
+      for (int h = 0; h < halves; ++h) {
+        const uint32_t hi = tmem + (uint32_t)(buf * 2 + h) * rcw, rest = tmem + 4u * rcw + (uint32_t)h * 2u * rcw;
+        for (int k = 0; k < (m + 15) / 16; ++k) {
+          const uint64_t xd = smem_desc_sw128(st + (uint32_t)(h * 16384 + k * 2048), 8192, 1024);
+          umma_bf16(hi, xd, smem_desc_sw128(v + (uint32_t)k * 2048u, 8192, 1024), id_hi, k ? 1u : 0u);
+          umma_bf16(rest, xd, smem_desc_sw128(v + 8192u + (uint32_t)k * 2048u, 8192, 1024), id_rest, (s | k) ? 1u : 0u);
+        }
+      }
+      last = s;
       umma_commit(ring.empty_bar());
+      umma_commit(acc_full + 8u * buf);
       ring.next();
     }
-    if (any) {
-      umma_commit(done_bar);
-      if (!ok) mbar_wait_bounded(done_bar, 0, nullptr);
-    }
+    if (!ok && last >= 0) mbar_wait_bounded(acc_full + 8u * (last & 1), (uint32_t)((last >> 1) & 1), nullptr);
   }
   __syncwarp();
 
@@ -632,31 +672,64 @@ __global__ void __launch_bounds__(kReqThreads) requests_grads_kernel(
   float* s_part = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
     const int quarter = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    float acc[2][NI][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[h][i][j] = 0.f;
     bool ok = true;
-    if (steps > 0) {
-      ok = mbar_wait_bounded(done_bar, 0, abort_flag);
-      tc_fence_after();
-    }
-    for (int h = 0; h < halves; ++h)
-      for (int j = 0; j < rc; j += 16) {
-        uint32_t v[3][16];
-        if (steps > 0 && ok) {
-          const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(h * 3 * rc + j);
-#pragma unroll
-          for (int part = 0; part < 3; ++part) tmem_ld_32x32b_x16(t + (uint32_t)(part * rc), v[part]);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int part = 0; part < 3; ++part)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[part][i] = 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s_part[(j + i) * kGradCols + h * 128 + quarter * 32 + lane] =
-              __uint_as_float(v[0][i]) + (__uint_as_float(v[1][i]) + __uint_as_float(v[2][i]));
+    for (int s = 0; s <= steps && steps > 0; ++s) {
+      // the stages' hi products, and behind the last one mid | lo
+      const bool rest = s == steps;
+      const int buf = s & 1;
+      if (!rest) {
+        ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag);
+        __syncwarp();
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h >= halves) break;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (16 * i >= rc) break;
+          uint32_t v[16];
+          if (!rest) {
+            tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * i, v);
+            tmem_ld_wait();
+          } else {
+            uint32_t w[16];
+            const uint32_t at = lanes + 4u * rcw + (uint32_t)h * 2u * rcw + 16u * i;
+            tmem_ld_32x32b_x16(at, v);
+            tmem_ld_32x32b_x16(at + (uint32_t)rc, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[h][i][j] += __uint_as_float(v[j]);
+        }
+      }
+      if (!rest) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
+      }
+    }
     tc_fence_before();
+    named_bar_sync(1, 128);                      // the sums lie over the stages
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (h < halves && 16 * i < rc)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s_part[(16 * i + j) * kGradCols + h * 128 + quarter * 32 + lane] = acc[h][i][j];
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
