@@ -297,6 +297,13 @@ cudaError_t set_deploy_attrs() {
   return fa.maxThreadsPerBlock >= kDeployThreads ? cudaSuccess : cudaErrorLaunchOutOfResources;
 }
 
+template <int NB, bool kTall>
+cudaError_t set_muon_attrs() {
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(muon_gram64_kernel<NB, kTall>, at, Gram64<NB>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(muon_poly64_kernel<NB, kTall>, at, Poly64<NB>::kSmem);
+  return e;
+}
 constexpr int kReqSmemMax = 226 * 1024;
 cudaError_t set_requests_attrs() {
   const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
@@ -307,6 +314,14 @@ cudaError_t set_requests_attrs() {
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_expand_kernel, at, kReqSmemMax);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel<1>, at, kReqSmemMax);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_grads_kernel<4>, at, kReqSmemMax);
+  if (e == cudaSuccess) e = set_muon_attrs<2, false>();
+  if (e == cudaSuccess) e = set_muon_attrs<2, true>();
+  if (e == cudaSuccess) e = set_muon_attrs<4, false>();
+  if (e == cudaSuccess) e = set_muon_attrs<4, true>();
+  if (e == cudaSuccess) e = set_muon_attrs<6, false>();
+  if (e == cudaSuccess) e = set_muon_attrs<6, true>();
+  if (e == cudaSuccess) e = set_muon_attrs<8, false>();
+  if (e == cudaSuccess) e = set_muon_attrs<8, true>();
   return e;
 }
 

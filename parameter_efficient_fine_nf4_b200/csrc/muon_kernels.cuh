@@ -53,6 +53,414 @@ __device__ __forceinline__ float muon_u(const MuonArgs& p, float g, float m_new)
   return p.nesterov ? __fmaf_rn(p.mu, m_new, g) : m_new;
 }
 
+// ---------------------------------------------------------- ranks up to 64
+// Three kernels: Gram matrix (with the momentum update), polynomial, product.
+// The 64-bit products go through the double-precision tensor instruction
+// m8n8k4 (A: row lane / 4, k = lane % 4; B: column lane / 4, k = lane % 4; D: row
+// lane / 4, columns 2 (lane % 4) + {0, 1}).  NB = rp / 8 blocks of 8.
+__device__ __forceinline__ void dmma(double (&d)[2], double a, double b) {
+  asm("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+      : "+d"(d[0]), "+d"(d[1])
+      : "d"(a), "d"(b));
+}
+
+// N consecutive floats, `have` of them inside the matrix (0 elsewhere); vec:
+// the address is 16-byte aligned whenever all of a group of four are inside.
+template <int N>
+__device__ __forceinline__ void load_run(const float* p, int64_t have, bool vec, float (&v)[N]) {
+  // from L2: a kernel that reads ahead of its wait must not see an older line
+  if (N % 4 == 0 && vec && have >= N) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(p) + i);
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < have ? __ldcg(p + i) : 0.f;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_run(float* p, int64_t have, bool vec, const float (&v)[N]) {
+  if (N % 4 == 0 && vec && have >= N) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < have) p[i] = v[i];
+  }
+}
+
+// Partial Gram matrices.  Every warp takes 16 long-side elements at a time and
+// multiplies all pairs of 8-row blocks (upper triangle) from registers: the
+// sum over the long side may run in any order, so a lane's four k-steps are
+// four consecutive elements (wide), and a block may hold any 8 rows, so a
+// lane's rows are NB consecutive ones (tall: block b, row lane / 4 is short
+// index NB (lane / 4) + b).  Loads are 16 bytes and nothing is staged.  The
+// warps of a cluster are then added in a fixed order; one partial per cluster.
+// part: [matrix][cluster][tile][8][8], tiles (i, j >= i) row by row.
+constexpr int kGram64Threads = 256;
+template <int NB>
+struct Gram64 {
+  static constexpr int kTiles = NB * (NB + 1) / 2;
+  static constexpr int kSmem = kGram64Threads / 32 * kTiles * 64 * 8;
+};
+template <int NB, bool kTall>
+__global__ void __launch_bounds__(kGram64Threads) muon_gram64_kernel(const MuonArgs p, int csize) {
+  constexpr int kTiles = Gram64<NB>::kTiles, kWarps = kGram64Threads / 32;
+  extern __shared__ __align__(16) double s_acc[];          // [warp][tile * 64]
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hi = lane >> 2, lo = lane & 3;
+  const int64_t mat = blockIdx.y, base = mat * (int64_t)p.r * p.len;
+  const int64_t blocks = (p.len + 15) / 16;
+  double acc[kTiles][2];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = 0.0;
+  for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < blocks; b += (int64_t)gridDim.x * kWarps) {
+    float u[NB][4];                                        // [block of 8][k-step]
+    if (!kTall) {
+      const bool vec = (p.len & 3) == 0;
+      float g[NB][4], m[NB][4];
+      const int64_t c = b * 16 + 4 * lo;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int row = 8 * i + hi;
+        const int64_t have = row < p.r ? p.len - c : 0, at = base + (int64_t)min(row, p.r - 1) * p.len + c;
+        load_run<4>(p.g + at, have, vec, g[i]);
+        load_run<4>(p.m + at, have, vec, m[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int row = 8 * i + hi;
+        const int64_t have = row < p.r ? p.len - c : 0, at = base + (int64_t)min(row, p.r - 1) * p.len + c;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          m[i][s] = __fmaf_rn(p.mu, m[i][s], g[i][s]);
+          u[i][s] = muon_u(p, g[i][s], m[i][s]);
+        }
+        store_run<4>(p.m + at, have, vec, m[i]);
+      }
+    } else {
+      const bool vec = (p.r & 3) == 0;
+      float g[4][NB], m[4][NB];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int64_t c = b * 16 + 4 * s + lo;
+        const int64_t have = c < p.len ? p.r - NB * hi : 0, at = base + min(c, p.len - 1) * p.r + NB * hi;
+        load_run<NB>(p.g + at, have, vec, g[s]);
+        load_run<NB>(p.m + at, have, vec, m[s]);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int64_t c = b * 16 + 4 * s + lo;
+        const int64_t have = c < p.len ? p.r - NB * hi : 0, at = base + min(c, p.len - 1) * p.r + NB * hi;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          m[s][i] = __fmaf_rn(p.mu, m[s][i], g[s][i]);
+          u[i][s] = muon_u(p, g[s][i], m[s][i]);
+        }
+        store_run<NB>(p.m + at, have, vec, m[s]);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      double f[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) f[i] = (double)u[i][s];
+      int t = 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = i; j < NB; ++j, ++t) dmma(acc[t], f[i], f[j]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+    *reinterpret_cast<double2*>(s_acc + (warp * kTiles + t) * 64 + hi * 8 + 2 * lo) = make_double2(acc[t][0], acc[t][1]);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kTiles * 64; e += kGram64Threads) {
+    double v = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += s_acc[w * kTiles * 64 + e];
+    s_acc[e] = v;                                          // only this thread reads or writes entry e of warp 0
+  }
+  if (csize > 1) cluster_sync();
+  else __syncthreads();
+  const int q = (int)(blockIdx.x % csize);
+  double* out = p.part + (mat * (gridDim.x / csize) + blockIdx.x / csize) * (int64_t)(kTiles * 64);
+  const uint32_t s0 = smem_u32(s_acc);
+  for (int e = q * kGram64Threads + threadIdx.x; e < kTiles * 64; e += csize * kGram64Threads) {
+    double v = 0.0;
+    for (int c = 0; c < csize; ++c) {
+      double x;
+      if (csize > 1)
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(mapa_shared(s0 + 8u * e, (uint32_t)c)) : "memory");
+      else
+        x = s_acc[e];
+      v += x;
+    }
+    out[e] = v;
+  }
+  if (csize > 1) cluster_sync();
+}
+
+// R0 from the partials, then `steps` rounds of the quintic's polynomial, all in
+// shared memory: a cluster of NB CTAs, each with 8 rows.  Q R needs R whole and
+// the CTA's own rows of Q, then R Q R and P Q need Q whole, so Q and R are
+// exchanged once each per round (every CTA writes its rows into every other's
+// copy); a product of 8 rows is one 8 x 8 block per warp.  Bound by the
+// latency of these exchanges.
+template <int NB>
+struct Poly64 {
+  static constexpr int kRp = 8 * NB, kPitch = kRp + 4;     // pitch of 4 mod 16: fragments without bank conflicts
+  static constexpr int kThreads = 32 * NB;
+  static constexpr int kSmem = (2 * kRp + 4 * 8) * kPitch * 8;
+};
+template <int NB>
+__device__ __forceinline__ void poly_product(double (&d)[2], const double* rows, const double* sym) {
+  // two chains hide half of the instruction's latency
+  double e[2] = {0.0, 0.0};
+  d[0] = d[1] = 0.0;
+#pragma unroll
+  for (int k = 0; k < 2 * NB; k += 2) {
+    dmma(d, rows[4 * k], sym[4 * k]);
+    dmma(e, rows[4 * k + 4], sym[4 * k + 4]);
+  }
+  d[0] += e[0];
+  d[1] += e[1];
+}
+template <int NB>
+__device__ __forceinline__ void poly_spread(const double* at, const double (&d)[2]) {
+  const uint32_t a = smem_u32(at);
+#pragma unroll
+  for (int c = 0; c < NB; ++c)
+    asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(mapa_shared(a, (uint32_t)c)), "d"(d[0]), "d"(d[1]) : "memory");
+}
+template <int NB, bool kTall>
+__global__ void __launch_bounds__(Poly64<NB>::kThreads) muon_poly64_kernel(const MuonArgs p, int parts, int steps) {
+  using C = Poly64<NB>;
+  constexpr int kTiles = Gram64<NB>::kTiles;
+  extern __shared__ __align__(16) double s_mat[];
+  double* R = s_mat;                               // [rp][pitch]
+  double* Q = R + C::kRp * C::kPitch;
+  double* H = Q + C::kRp * C::kPitch;              // 8 rows
+  double* P[2] = {H + 8 * C::kPitch, H + 16 * C::kPitch};
+  __shared__ double s_inv;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int q = (int)cluster_ctarank();
+  const int64_t mat = blockIdx.x / NB;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
+  cluster_sync();                                  // every CTA runs before its memory is written
+  // this CTA's 8 rows of the Gram matrix: the sum of the partials
+  const double* part = p.part + mat * parts * (int64_t)(kTiles * 64);
+  for (int e = threadIdx.x; e < 8 * C::kRp; e += C::kThreads) {
+    const int i = 8 * q + e / C::kRp, j = e % C::kRp;
+    // block and row within it of a short index
+    const int bi = kTall ? i % NB : i / 8, ri = kTall ? i / NB : i % 8, bj = kTall ? j % NB : j / 8, rj = kTall ? j / NB : j % 8;
+    const bool up = bi <= bj;
+    const int x = up ? bi : bj, y = up ? bj : bi;
+    const int at = (x * NB - x * (x - 1) / 2 + y - x) * 64 + (up ? ri * 8 + rj : rj * 8 + ri);
+    double v = 0.0;
+    for (int k = 0; k < parts; ++k) v += part[k * kTiles * 64 + at];
+    const uint32_t to = smem_u32(R + i * C::kPitch + j);
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(to, (uint32_t)c)), "d"(v) : "memory");
+  }
+  cluster_sync();
+  if (warp == 0) {
+    double t = 0.0;
+    for (int i = lane; i < C::kRp; i += 32) t += R[i * C::kPitch + i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (lane == 0) s_inv = 1.0 / (sqrt(t) + p.eps);
+  }
+  __syncthreads();
+  const double inv = s_inv;
+  for (int e = threadIdx.x; e < C::kRp * C::kRp; e += C::kThreads) R[e / C::kRp * C::kPitch + e % C::kRp] *= inv * inv;
+  __syncthreads();
+
+  // fragment addresses: this CTA's rows of R, Q; a warp's 8 columns (rows of a symmetric matrix)
+  const int mine = (8 * q + hi) * C::kPitch, col = (8 * warp + hi) * C::kPitch;
+  const int out = hi * C::kPitch + 8 * warp + 2 * lo, at = 8 * q * C::kPitch + out;
+  int cur = 0;
+  for (int it = 0; it < steps; ++it) {
+    const bool last = it == steps - 1;
+    double d[2];
+    poly_product<NB>(d, R + mine + lo, R + col + lo);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      d[e] = p.c * d[e] + p.b * R[at + e];
+      if (8 * q + hi == 8 * warp + 2 * lo + e) d[e] += p.a;
+    }
+    poly_spread<NB>(Q + at, d);
+    if (it == 0) {                                 // P = Q; it carries the norm of x0 = u inv
+      P[0][out] = inv * d[0];
+      P[0][out + 1] = inv * d[1];
+    }
+    if (!last) {
+      __syncthreads();                             // this CTA's rows of Q
+      poly_product<NB>(d, Q + mine + lo, R + col + lo);
+      H[out] = d[0];
+      H[out + 1] = d[1];
+    }
+    cluster_sync();                                // Q everywhere
+    if (it > 0) {
+      poly_product<NB>(d, P[cur] + hi * C::kPitch + lo, Q + col + lo);
+      P[cur ^ 1][out] = d[0];
+      P[cur ^ 1][out + 1] = d[1];
+      cur ^= 1;
+    }
+    if (!last) {
+      poly_product<NB>(d, H + hi * C::kPitch + lo, Q + col + lo);
+      poly_spread<NB>(R + at, d);
+      cluster_sync();                              // R everywhere
+    }
+  }
+  __syncthreads();
+  double* to = p.P + (mat * C::kRp + 8 * q) * (int64_t)C::kRp;
+  for (int e = threadIdx.x; e < 8 * C::kRp; e += C::kThreads) to[e] = P[cur][e / C::kRp * C::kPitch + e % C::kRp];
+}
+
+// x = P u and the update.  A warp holds 32 long-side elements of u as 64-bit
+// fragments and goes through P's rows, kept in shared memory.  Which k-step an
+// index of the inner sum falls in, and which column of a block a long-side
+// (wide) or short-side (tall) index is, is chosen so that every lane reads and
+// writes runs of consecutive floats.
+constexpr int kApply64Threads = 128;
+template <int NB, bool kTall>
+__global__ void __launch_bounds__(kApply64Threads) muon_apply64_kernel(const MuonArgs p) {
+  constexpr int kRp = 8 * NB, kPitch = kRp + 4, KS = 2 * NB;
+  __shared__ __align__(16) double s_p[kRp * kPitch];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
+  const int64_t mat = blockIdx.y, base = mat * (int64_t)p.r * p.len;
+  const bool vec = kTall ? (p.r & 3) == 0 : (p.len & 3) == 0;
+  const int64_t blocks = (p.len + 31) / 32;
+  bool ready = false;
+  for (int64_t b0 = (int64_t)blockIdx.x * 4; b0 < blocks; b0 += (int64_t)gridDim.x * 4) {
+    const int64_t b = b0 + warp;
+    double f[4][KS];                               // [8 long-side elements][k-step]
+    if (b < blocks) {
+      // the momentum was written two launches ago: it may be read before the
+      // wait for the polynomial
+      if (!kTall) {
+        // k-step ks, lane: short index 4 ks + lo; block cb, lane: long index 4 hi + cb
+        const int64_t c = b * 32 + 4 * hi;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int row = 4 * k + lo;
+          const int64_t have = row < p.r ? p.len - c : 0, at = base + (int64_t)min(row, p.r - 1) * p.len + c;
+          float g[4], m[4];
+          load_run<4>(p.g + at, have, vec, g);
+          load_run<4>(p.m + at, have, vec, m);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e][k] = (double)muon_u(p, g[e], m[e]);
+        }
+      } else {
+        // k-step ks, lane: short index KS lo + ks; block cb, lane: long index 8 cb + hi
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t c = b * 32 + 8 * e + hi;
+          const int64_t have = c < p.len ? p.r - KS * lo : 0, at = base + min(c, p.len - 1) * p.r + KS * lo;
+          float g[KS], m[KS];
+          load_run<KS>(p.g + at, have, vec, g);
+          load_run<KS>(p.m + at, have, vec, m);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) f[e][k] = (double)muon_u(p, g[k], m[k]);
+        }
+      }
+    }
+    if (!ready) {
+      griddep_wait();
+      griddep_launch_dependents();
+      const double* P = p.P + mat * kRp * kRp;
+      for (int e = threadIdx.x; e < kRp * kRp; e += kApply64Threads) {
+        const int i = e / kRp, j = e % kRp;
+        if (!kTall) {
+          s_p[i * kPitch + j] = P[e];
+        } else {
+          // row: block ib, column n of short index i = 2 NB (n / 2) + 2 ib + n % 2; column: k-step order
+          const int n = i / (2 * NB) * 2 + (i & 1), ib = i % (2 * NB) / 2;
+          s_p[(8 * ib + n) * kPitch + 4 * (j % KS) + j / KS] = P[e];
+        }
+      }
+      __syncthreads();
+      ready = true;
+    }
+    if (b >= blocks) continue;
+#pragma unroll 1
+    for (int ib = 0; ib < NB; ib += 2) {
+      float w[4][4] = {};                          // master values
+      int64_t at[4];
+      int64_t have[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!kTall) {
+          // rows ib and ib + 1, two runs of four each: e = 2 (row block) + run
+          const int row = 8 * (ib + e / 2) + hi;
+          const int64_t c = b * 32 + 8 * lo + 4 * (e & 1);
+          have[e] = row < p.r ? p.len - c : 0;
+          at[e] = base + (int64_t)min(row, p.r - 1) * p.len + c;
+        } else {
+          const int64_t c = b * 32 + 8 * e + hi;
+          const int i = 2 * NB * lo + 2 * ib;
+          have[e] = c < p.len ? p.r - i : 0;
+          at[e] = base + min(c, p.len - 1) * p.r + i;
+        }
+        load_run<4>(p.master + at[e], have[e], vec, w[e]);
+      }
+      double d[2][4][2] = {};                      // [row block][8 long-side elements][2]
+      const double* s0 = s_p + (8 * ib + hi) * kPitch + lo;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const double x = s0[4 * k], y = s0[8 * kPitch + 4 * k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!kTall) {
+            dmma(d[0][e], x, f[e][k]);
+            dmma(d[1][e], y, f[e][k]);
+          } else {
+            dmma(d[0][e], f[e][k], x);
+            dmma(d[1][e], f[e][k], y);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // wide: long index 4 (2 lo + h) + cb, h = e & 1; tall: short index 2 NB lo + 2 (ib + i / 2) + i % 2
+          const float x = (float)(kTall ? d[i / 2][e][i & 1] : d[e / 2][i][e & 1]);
+          w[e][i] = __fmaf_rn(p.keep, w[e][i], -__fmul_rn(p.step, x));
+        }
+        store_run<4>(p.master + at[e], have[e], vec, w[e]);
+        if (vec && have[e] >= 4) {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(w[e][0], w[e][1]), c = __floats2bfloat162_rn(w[e][2], w[e][3]);
+          *reinterpret_cast<uint2*>(p.w16 + at[e]) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < have[e]) {
+              const __nv_bfloat16 h = __float2bfloat16_rn(w[e][i]);
+              p.w16[at[e] + i] = *reinterpret_cast<const uint16_t*>(&h);
+            }
+        }
+      }
+    }
+  }
+  if (!ready) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+}
+
+// ------------------------------------------------------------ ranks above 64
 // m = mu m + g over all elements.
 __global__ void __launch_bounds__(256) muon_momentum_kernel(float* __restrict__ m, const float* __restrict__ g, float mu,
                                                             int64_t count) {
