@@ -9,6 +9,7 @@ Names mirror the C entry points.  bf16 tensors are ``torch.bfloat16``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -528,54 +529,54 @@ def lora_adam_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Ten
 
 # ------------------------------------------------- many adapters at once (requests)
 class _On:
-    """The device a call runs on: makes it current, allocates on the call's
-    stream (so that a temporary's memory is reused in that stream's order) and
-    restores both."""
+    """The device a call runs on: gives the raw stream, makes the device
+    current, allocates on the call's stream (so that a temporary's memory is
+    reused in that stream's order) and restores both."""
 
-    __slots__ = ("device", "stream", "guard", "outer")
+    __slots__ = ("device", "stream", "held")
 
     def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+        self.device, self.stream, self.held = device, stream, None
 
     def __enter__(self):
-        self.guard = self.outer = None
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        if self.stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        if self.stream.device != self.device:
-            if self.guard is not None:
-                self.guard.__exit__(None, None, None)
-            raise ValueError(f"stream of {self.stream.device} for tensors on {self.device}")
-        self.outer = torch.cuda.stream(self.stream)
-        self.outer.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        device, stream = self.device, self.stream
+        here = device.index == torch._C._cuda_getDevice()
+        if stream is None and here:              # the usual call: nothing to switch
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        self.held = contextlib.ExitStack()
+        if not here:
+            self.held.enter_context(torch.cuda.device(device))
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(device.index)
+        self.held.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream
 
     def __exit__(self, *exc):
-        if self.outer is not None:
-            self.outer.__exit__(*exc)
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        if self.held is not None:
+            self.held.close()
+
+
+def _refuse(t: torch.Tensor, dtype, shape, device, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}, got {t.device}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _need_on(t: torch.Tensor, dtype, shape, device, name) -> int:
     """Data pointer of a contiguous tensor of this type and shape on this device."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(t, dtype, shape, device, name)
     return t.data_ptr()
 
 
-def _need_ws(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
-    if ws is None:
-        return workspace(nbytes, device)
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+def _need_ws(ws: torch.Tensor, device) -> torch.Tensor:
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws: must be a contiguous uint8 tensor on {device}")
     return ws
 
@@ -620,6 +621,7 @@ class AdapterPool:
         self.scale = torch.tensor([a / r for a, r in zip(alphas, ranks)], dtype=torch.float32, device=device)
         self._c = _Pool(self.A.data_ptr(), self.Bt.data_ptr(), self.first.data_ptr(), self.rank.data_ptr(),
                         self.scale.data_ptr(), rows, k, d, self.n, self.width)
+        self._ref = ctypes.byref(self._c)
 
     @property
     def cstruct(self) -> _Pool:
@@ -661,6 +663,7 @@ class RequestPlan:
         self._c = _Requests(*(t.data_ptr() or self._tiles.data_ptr()
                               for t in (self.starts, self.idx, self.order, self.seg, self._tile_first, self._tiles)),
                             T, n_req, n)
+        self._ref = ctypes.byref(self._c)
 
     @property
     def cstruct(self) -> _Requests:
@@ -673,7 +676,7 @@ def lora_requests_plan(lens: torch.Tensor, adapters: torch.Tensor, plan: Request
     ap = _need_on(adapters, torch.int32, (plan.n_req,), plan.device, "adapters")
     with _On(plan.device, stream) as st:
         _check(lib().lora_requests_plan(lp or plan._tiles.data_ptr(), ap or plan._tiles.data_ptr(),
-                                        ctypes.byref(plan.cstruct), st), "lora_requests_plan")
+                                        plan._ref, st), "lora_requests_plan")
     return plan
 
 
@@ -685,11 +688,11 @@ def _need_match(pool: AdapterPool, plan: RequestPlan):
 
 
 def lora_requests_fwd_workspace_bytes(pool: AdapterPool, plan: RequestPlan) -> int:
-    return lib().lora_requests_fwd_workspace_bytes(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct))
+    return lib().lora_requests_fwd_workspace_bytes(pool._ref, plan._ref)
 
 
 def lora_requests_bwd_workspace_bytes(pool: AdapterPool, plan: RequestPlan) -> int:
-    return lib().lora_requests_bwd_workspace_bytes(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct))
+    return lib().lora_requests_bwd_workspace_bytes(pool._ref, plan._ref)
 
 
 def lora_requests_fwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, base: Optional[torch.Tensor] = None,
@@ -709,10 +712,8 @@ def lora_requests_fwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, bas
             U_save = torch.zeros(T, pool.width, dtype=torch.float32, device=dev)
         yp = _need_on(Y, bf, (T, pool.d), dev, "Y")
         up = None if U_save is None else _need_on(U_save, torch.float32, (T, pool.width), dev, "U_save")
-        if ws is None:
-            ws = workspace(lora_requests_fwd_workspace_bytes(pool, plan), dev)
-        ws = _need_ws(ws, 0, dev)
-        _check(lib().lora_requests_fwd(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct), xp, bp, yp, up,
+        ws = workspace(lora_requests_fwd_workspace_bytes(pool, plan), dev) if ws is None else _need_ws(ws, dev)
+        _check(lib().lora_requests_fwd(pool._ref, plan._ref, xp, bp, yp, up,
                                        ws.data_ptr(), ws.numel(), st), "lora_requests_fwd")
     return Y, U_save
 
@@ -736,10 +737,8 @@ def lora_requests_bwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, U_s
         dxp = _need_on(dX, bf, (T, pool.k), dev, "dX")
         dap = _need_on(dA, f32, (pool.rows, pool.k), dev, "dA")
         dbp = _need_on(dBt, f32, (pool.rows, pool.d), dev, "dBt")
-        if ws is None:
-            ws = workspace(lora_requests_bwd_workspace_bytes(pool, plan), dev)
-        ws = _need_ws(ws, 0, dev)
-        _check(lib().lora_requests_bwd(ctypes.byref(pool.cstruct), ctypes.byref(plan.cstruct), xp, up, gp, bp, dxp, dap,
+        ws = workspace(lora_requests_bwd_workspace_bytes(pool, plan), dev) if ws is None else _need_ws(ws, dev)
+        _check(lib().lora_requests_bwd(pool._ref, plan._ref, xp, up, gp, bp, dxp, dap,
                                        dbp, ws.data_ptr(), ws.numel(), st), "lora_requests_bwd")
     return dX, dA, dBt
 
@@ -771,9 +770,7 @@ def lora_muon_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Ten
             raise ValueError("coefs: expected three")
         cs = (ctypes.c_float * 3)(*[float(c) for c in coefs])
     with _On(dev, stream) as st:
-        if ws is None:
-            ws = workspace(lora_muon_workspace_bytes(n, rows, cols), dev)
-        ws = _need_ws(ws, 0, dev)
+        ws = workspace(lora_muon_workspace_bytes(n, rows, cols), dev) if ws is None else _need_ws(ws, dev)
         _check(lib().lora_muon_step(*ptrs, n, rows, cols, float(lr), float(momentum), int(bool(nesterov)), float(scale),
                                     float(weight_decay), float(eps), int(steps),
                                     None if cs is None else ctypes.addressof(cs), ws.data_ptr(), ws.numel(), st),
