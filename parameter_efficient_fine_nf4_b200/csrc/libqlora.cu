@@ -308,6 +308,10 @@ constexpr int kReqSmemMax = 226 * 1024;
 cudaError_t set_requests_attrs() {
   const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(requests_plan_kernel, at, (int)plan_smem_bytes(kReqMax, kReqMax));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_few_kernel, at, (int)sizeof(FewShared));
+  if (e == cudaSuccess && cudaFuncSetAttribute(requests_few_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                              cudaSuccess)
+    cudaGetLastError();                        // few_cluster16_fit then finds no such cluster
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<2>, at, kReqSmemMax);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<4>, at, kReqSmemMax);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_shrink_kernel<8>, at, kReqSmemMax);
@@ -323,6 +327,33 @@ cudaError_t set_requests_attrs() {
   if (e == cudaSuccess) e = set_muon_attrs<8, false>();
   if (e == cudaSuccess) e = set_muon_attrs<8, true>();
   return e;
+}
+
+// Whether the device holds clusters of 16 few-token CTAs.
+bool few_cluster16_fit() {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = sizeof(FewShared);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 16;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, requests_few_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return n > 0;
+}
+bool g_dev_few16[kMaxDevices] = {false};
+bool few_cluster16() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_dev_few16[dev];
 }
 
 int ensure_device() {
@@ -354,6 +385,7 @@ int ensure_device() {
     return QLORA_ERR_CUDA;
   g_dev_pair_clusters[dev] = pair_clusters_on_device();
   small_cluster_fit(g_dev_cluster_fit[dev]);
+  g_dev_few16[dev] = few_cluster16_fit();
   g_dev_ctx[dev] = current_ctx_id();
   g_dev_ready[dev] = true;
   return QLORA_OK;

@@ -94,24 +94,30 @@ __global__ void __launch_bounds__(kPlanThreads) requests_plan_kernel(const PlanA
   int* s_tile = s_seg + p.n + 2;                 // n + 2
   const int tid = threadIdx.x;
   griddep_wait();
+  griddep_launch_dependents();
+  for (int i = tid; i < p.n_req; i += kPlanThreads) {
+    s_start[i] = max(0, p.lens[i]);
+    const int a = p.ids[i];
+    s_id[i] = (a >= 0 && a < p.n) ? a : p.n;
+  }
+  for (int g = tid; g < p.n + 2; g += kPlanThreads) s_seg[g] = 0;
+  __syncthreads();
 
   // first rows: a 64-bit sum, cut at T, so that no lengths can overflow it
   {
     const int per = (p.n_req + kPlanThreads - 1) / kPlanThreads;
     const int i0 = min(p.n_req, tid * per), i1 = min(p.n_req, i0 + per);
     long long sum = 0;
-    for (int i = i0; i < i1; ++i) sum += max(0, p.lens[i]);
+    for (int i = i0; i < i1; ++i) sum += s_start[i];
     long long total;
     long long run = block_exclusive<long long>(sum, s_warp64, total);
     for (int i = i0; i < i1; ++i) {
+      const int len = s_start[i];
       s_start[i] = (int)min(run, (long long)p.T);
-      run += max(0, p.lens[i]);
-      const int a = p.ids[i];
-      s_id[i] = (a >= 0 && a < p.n) ? a : p.n;
+      run += len;
     }
     if (tid == 0) s_start[p.n_req] = (int)min(total, (long long)p.T);
   }
-  for (int g = tid; g < p.n + 2; g += kPlanThreads) s_seg[g] = 0;
   __syncthreads();
   // tokens of each group (integer sums: their order does not matter)
   for (int i = tid; i < p.n_req; i += kPlanThreads) {
@@ -219,14 +225,22 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // Tiles of up to 8 tokens of one adapter.  A cluster of CTAs takes one tile:
 // each CTA sums U over its share of the K columns, the shares are added in
 // rank order over the cluster's shared memory, and each CTA then writes its
-// share of the N output columns.  One launch, X and the factors read once,
-// everything in fp32 on CUDA cores.
+// share of the N output columns.  One launch, the factors read once, all
+// arithmetic in fp32 on CUDA cores.
+//
+// The factors are what has to be read (a few tokens' X is nothing), so a
+// producer thread streams this CTA's part of both through a ring of TMA boxes,
+// 16 rows x 256 columns a stage: 48 KB are in flight per CTA from the first
+// moment, and the second factor arrives while the cluster still adds up U.
 constexpr int kFewTile = 8;
-constexpr int kFewThreads = 256;
+constexpr int kFewWarps = 8;                   // consumers; one more warp produces
+constexpr int kFewThreads = 32 * (kFewWarps + 1);
+constexpr int kFewRows = 16;                   // rows of a stage
+constexpr int kFewCols = 256;                  // columns of a stage
+constexpr int kFewStages = 6;
+constexpr int kFewStageBytes = kFewRows * kFewCols * 2;
 
 struct FewArgs {
-  const uint16_t* W1;      // rows x K
-  const uint16_t* W2;      // rows x N
   const uint16_t* X;       // T x K
   const uint16_t* base;    // T x N, or null (zero)
   uint16_t* out;           // T x N
@@ -238,153 +252,233 @@ struct FewArgs {
   PoolArgs pool;
 };
 
-// Rows of 8 consecutive bf16 values times NT tokens: acc[row][token] += w . x
+struct FewShared {
+  uint64_t full[kFewStages], empty[kFewStages], ready;
+  int abort_flag;
+  alignas(16) float part[256 * kFewTile];        // [row][token]: this CTA's share of U
+  alignas(16) float u[kFewTile * 256];           // [token][row]: scaled U
+  alignas(16) float red[kFewTile * kFewCols];    // the second half of the rows' sums
+  alignas(128) uint8_t ring[kFewStages * kFewStageBytes];
+};
+
+// One arrival on an mbarrier of any CTA of the cluster, releasing this CTA's
+// earlier shared-memory writes to its threads.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+struct FewRing {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kFewStages) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Stages of one factor for this CTA (one thread): for the first factor all
+// columns of 16 rows, then the next rows; for the second all rows of 256
+// columns.  Boxes of 8 rows: a stage's second one only where the rank has it.
+__device__ __forceinline__ bool few_produce(FewShared& s, FewRing& ring, int& issued, const CUtensorMap* w, int first, int rank,
+                                            int c0, int c1, bool rows_first) {
+  const int rb = (rank + kFewRows - 1) / kFewRows, cb = (c1 - c0 + kFewCols - 1) / kFewCols;
+  for (int i = 0; i < rb * cb; ++i) {
+    const int r = (rows_first ? i % rb : i / cb) * kFewRows, c = c0 + (rows_first ? i / rb : i % cb) * kFewCols;
+    const bool two = rank - r > 8;
+    const uint32_t full = smem_u32(&s.full[ring.at]);
+    if (!mbar_wait_bounded(smem_u32(&s.empty[ring.at]), ring.phase ^ 1u, &s.abort_flag)) return false;
+    mbar_arrive_expect_tx(full, two ? kFewStageBytes : kFewStageBytes / 2);
+    const uint32_t dst = smem_u32(s.ring) + (uint32_t)(ring.at * kFewStageBytes);
+    tma_load_2d(dst, w, full, c, first + r);
+    if (two) tma_load_2d(dst + kFewStageBytes / 2, w, full, c, first + r + 8);
+    ring.next();
+    ++issued;
+  }
+  return true;
+}
+
+// One value of every CTA of the cluster, added in rank order.
+template <int CS>
+__device__ __forceinline__ float few_cluster_sum(uint32_t at) {
+  float f[CS];
+#pragma unroll
+  for (int c = 0; c < CS; ++c) f[c] = ld_shared_cluster_f32(mapa_shared(at, (uint32_t)c));
+  float v = f[0];
+#pragma unroll
+  for (int c = 1; c < CS; ++c) v += f[c];
+  return v;
+}
+
+// The consumers' side of a tile (warps 0 .. 7).  X's values stay in L1.
 template <int NT>
-__device__ __forceinline__ void few_shrink(const FewArgs& p, const AdapterRows& ad, const int (&tok)[kFewTile], int k0,
-                                           int k1, float* s_part) {
-  constexpr int RB = NT >= 4 ? 2 : 4;          // rows per pass share the loaded x
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r0 = warp * RB; r0 < ad.rank; r0 += (kFewThreads / 32) * RB) {
-    float acc[RB][NT];
+__device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, const AdapterRows& ad, const int (&tok)[kFewTile],
+                                            int count, int q, int k0, int k1, int n0, int n1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rb = (ad.rank + kFewRows - 1) / kFewRows;
+  FewRing ring;
+  bool ok = true;
+  // U: a warp takes rows w and w + 8 of a stage, a lane 8 columns
+  for (int r = 0; r < ad.rank && ok; r += kFewRows) {
+    const bool two = r + warp + 8 < ad.rank;
+    float acc[2][NT];
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = 0.f;
+    for (int c = k0; c < k1; c += kFewCols) {
+      const int x0 = c + lane * 8;
+      const bool in = x0 < k1;
+      uint4 xv[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[i][t] = 0.f;
-    const uint16_t* w0 = p.W1 + (int64_t)(ad.first + r0) * p.K;
-#pragma unroll 2
-    for (int c = k0 + lane * 8; c < k1; c += 256) {
-      uint4 w[RB];
+      for (int t = 0; t < NT; ++t)
+        xv[t] = in ? __ldg(reinterpret_cast<const uint4*>(p.X + (int64_t)tok[t] * p.K + x0)) : make_uint4(0, 0, 0, 0);
+      ok = mbar_wait_bounded(smem_u32(&s.full[ring.at]), ring.phase, &s.abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      const uint8_t* st = s.ring + ring.at * kFewStageBytes + warp * (kFewCols * 2) + lane * 16;
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
-        w[i] = r0 + i < ad.rank ? __ldg(reinterpret_cast<const uint4*>(w0 + (int64_t)i * p.K + c)) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 2; ++i) {
+        if (in && r + warp + 8 * i < ad.rank) {
+          const uint4 w = *reinterpret_cast<const uint4*>(st + i * 8 * kFewCols * 2);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.X + (int64_t)tok[t] * p.K + c));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          for (int t = 0; t < NT; ++t) {
+            const uint32_t xs[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][t] = __fmaf_rn(bf_lo(ws[j]), bf_lo(xs[j]), acc[i][t]);
-            acc[i][t] = __fmaf_rn(bf_hi(ws[j]), bf_hi(xs[j]), acc[i][t]);
+            for (int j = 0; j < 4; ++j) {
+              acc[i][t] = __fmaf_rn(bf_lo(ws[j]), bf_lo(xs[j]), acc[i][t]);
+              acc[i][t] = __fmaf_rn(bf_hi(ws[j]), bf_hi(xs[j]), acc[i][t]);
+            }
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
+      ring.next();
     }
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int i = 0; i < 2; ++i) {
+      if (i == 1 && !two) break;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float v = acc[i][t];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == 0 && r0 + i < ad.rank) s_part[(r0 + i) * kFewTile + t] = v;
-      }
-  }
-}
-
-// out[tok][c..c+3] for this CTA's columns; RG groups of threads share the
-// adapter's rows and are summed in group order.
-template <int NT>
-__device__ __forceinline__ void few_expand(const FewArgs& p, const AdapterRows& ad, const int (&tok)[kFewTile], int count,
-                                           int n0, int n1, const float* s_u, float* s_red) {
-  const int cols4 = (n1 - n0) / 4;
-  int groups = 1;
-  while (groups < 8 && cols4 * groups * 2 <= kFewThreads) groups *= 2;
-  const int per = kFewThreads / groups;        // threads of a group
-  const int g = threadIdx.x / per, x = threadIdx.x % per;
-  for (int cb = 0; cb < cols4; cb += per) {
-    const int c4 = cb + x;
-    const bool ok = c4 < cols4;
-    const int c = n0 + c4 * 4;
-    float acc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
-    if (ok) {
-      const uint16_t* w = p.W2 + (int64_t)ad.first * p.N + c;
-#pragma unroll 4
-      for (int r = g; r < ad.rank; r += groups) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(w + (int64_t)r * p.N));
-        const float f[4] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y)};
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float u = s_u[r * kFewTile + t];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[t][j] = __fmaf_rn(u, f[j], acc[t][j]);
-        }
-      }
-    }
-    if (groups > 1) {
-      __syncthreads();
-      if (ok && g > 0) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          *reinterpret_cast<float4*>(s_red + (((g - 1) * NT + t) * per + x) * 4) =
-              make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-      }
-      __syncthreads();
-      if (ok && g == 0) {
-        for (int q = 1; q < groups; ++q)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float4 v = *reinterpret_cast<const float4*>(s_red + (((q - 1) * NT + t) * per + x) * 4);
-            acc[t][0] += v.x; acc[t][1] += v.y; acc[t][2] += v.z; acc[t][3] += v.w;
-          }
-      }
-    }
-    if (ok && g == 0) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t >= count) break;
-        const int64_t at = (int64_t)tok[t] * p.N + c;
-        uint2 b = make_uint2(0, 0);
-        if (p.base) b = *reinterpret_cast<const uint2*>(p.base + at);
-        uint2 o;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(bf_lo(b.x) + acc[t][0], bf_hi(b.x) + acc[t][1]);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(bf_lo(b.y) + acc[t][2], bf_hi(b.y) + acc[t][3]);
-        o.x = *reinterpret_cast<const uint32_t*>(&lo);
-        o.y = *reinterpret_cast<const uint32_t*>(&hi);
-        *reinterpret_cast<uint2*>(p.out + at) = o;
+        if (lane == 0 && r + warp + 8 * i < ad.rank) s.part[(r + warp + 8 * i) * kFewTile + t] = v;
       }
     }
   }
-}
-
-template <int NT>
-__device__ __forceinline__ void few_tile(const FewArgs& p, const AdapterRows& ad, const int (&tok)[kFewTile], int count,
-                                         int q, int csize, float* s_part, float* s_u, float* s_red) {
-  // shares of the columns: whole 16-byte words
-  const int kc = ((p.K / 8 + csize - 1) / csize) * 8, nc = ((p.N / 8 + csize - 1) / csize) * 8;
-  const int k0 = min(p.K, q * kc), k1 = min(p.K, k0 + kc);
-  const int n0 = min(p.N, q * nc), n1 = min(p.N, n0 + nc);
-  few_shrink<NT>(p, ad, tok, k0, k1, s_part);
-  cluster_sync();
-  const uint32_t part = smem_u32(s_part);
-  for (int e = threadIdx.x; e < ad.rank * NT; e += kFewThreads) {
+  // base comes in while the cluster meets
+  const int g = threadIdx.x >> 7, x2 = (threadIdx.x & 127) * 2;     // half of a stage's rows, 2 columns
+  uint32_t base[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    base[t] = g == 0 && p.base && t < count && n0 + x2 < n1
+                  ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tok[t] * p.N + n0 + x2) : 0u;
+  // the producer goes on streaming, so the consumers meet on a barrier of their own
+  named_bar_sync(1, 32 * kFewWarps);
+  if (p.csize > 1) {
+    if (threadIdx.x < p.csize) mbar_arrive_cluster(mapa_shared(smem_u32(&s.ready), threadIdx.x));
+    ok = mbar_wait_bounded<true>(smem_u32(&s.ready), 0, &s.abort_flag) && ok;
+    __syncwarp();
+  }
+  const uint32_t part = smem_u32(s.part);
+  for (int e = threadIdx.x; e < ad.rank * NT; e += 32 * kFewWarps) {
     const int r = e / NT, t = e % NT;
-    float v = 0.f;
-    for (int c = 0; c < csize; ++c)
-      v += ld_shared_cluster_f32(mapa_shared(part + (uint32_t)(r * kFewTile + t) * 4u, (uint32_t)c));
-    s_u[r * kFewTile + t] = ad.scale * v;
+    const uint32_t at = part + (uint32_t)(r * kFewTile + t) * 4u;
+    const float v = p.csize == 16 ? few_cluster_sum<16>(at) : p.csize == 8 ? few_cluster_sum<8>(at)
+                    : p.csize == 4 ? few_cluster_sum<4>(at) : p.csize == 2 ? few_cluster_sum<2>(at) : few_cluster_sum<1>(at);
+    s.u[t * 256 + r] = ad.scale * v;
     if (q == 0 && t < count) {
       if (p.U) p.U[(int64_t)tok[t] * p.width + r] = v;
       if (p.sU) p.sU[(int64_t)tok[t] * p.width + r] = ad.scale * v;
     }
   }
-  __syncthreads();
-  few_expand<NT>(p, ad, tok, count, n0, n1, s_u, s_red);
+  // rows up to the stage's 16 multiply whatever the stage holds: make that nothing
+  for (int e = threadIdx.x; e < (rb * kFewRows - ad.rank) * NT; e += 32 * kFewWarps)
+    s.u[(e % NT) * 256 + ad.rank + e / NT] = 0.f;
+  named_bar_sync(1, 32 * kFewWarps);
+  for (int c = n0; c < n1; c += kFewCols) {
+    const int x = c + x2;
+    const bool in = x < n1;
+    if (c > n0) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        base[t] = g == 0 && p.base && t < count && in ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tok[t] * p.N + x) : 0u;
+    }
+    float acc[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
+    for (int r = 0; r < ad.rank && ok; r += kFewRows) {
+      ok = mbar_wait_bounded(smem_u32(&s.full[ring.at]), ring.phase, &s.abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      if (in && r + 8 * g < ad.rank) {
+        const uint8_t* st = s.ring + ring.at * kFewStageBytes + 8 * g * (kFewCols * 2) + x2 * 2;
+        const int m = min(8, ad.rank - r - 8 * g);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < m ? *reinterpret_cast<const uint32_t*>(st + i * kFewCols * 2) : 0u;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float4 a = *reinterpret_cast<const float4*>(s.u + t * 256 + r + 8 * g);
+          const float4 b = *reinterpret_cast<const float4*>(s.u + t * 256 + r + 8 * g + 4);
+          const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[t][0] = __fmaf_rn(u[i], bf_lo(w[i]), acc[t][0]);
+            acc[t][1] = __fmaf_rn(u[i], bf_hi(w[i]), acc[t][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
+      ring.next();
+    }
+    if (rb * kFewRows > 8 && ad.rank > 8) {      // the second half's sums
+      named_bar_sync(1, 32 * kFewWarps);
+      if (g == 1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<float2*>(s.red + t * kFewCols + x2) = make_float2(acc[t][0], acc[t][1]);
+      }
+      named_bar_sync(1, 32 * kFewWarps);
+      if (g == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 v = *reinterpret_cast<const float2*>(s.red + t * kFewCols + x2);
+          acc[t][0] += v.x;
+          acc[t][1] += v.y;
+        }
+      }
+    }
+    if (g == 0 && in) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (t >= count) break;
+        const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(base[t]) + acc[t][0], bf_hi(base[t]) + acc[t][1]);
+        *reinterpret_cast<uint32_t*>(p.out + (int64_t)tok[t] * p.N + x) = *reinterpret_cast<const uint32_t*>(&o);
+      }
+    }
+  }
 }
 
-__global__ void __launch_bounds__(kFewThreads) requests_few_kernel(const FewArgs p) {
-  __shared__ __align__(16) float s_part[256 * kFewTile];
-  __shared__ __align__(16) float s_u[256 * kFewTile];
-  __shared__ __align__(16) float s_red[kFewTile * kFewThreads * 4];
+__global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __grid_constant__ CUtensorMap w1,
+                                                                      const __grid_constant__ CUtensorMap w2,
+                                                                      const __grid_constant__ FewArgs p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  FewShared& s = *reinterpret_cast<FewShared*>(smem_raw);
   const int csize = p.csize;                   // CTAs of a cluster
   const int q = (int)(blockIdx.x % csize);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), kFewWarps);
+    }
+    mbar_init(smem_u32(&s.ready), (uint32_t)csize);
+    s.abort_flag = 0;
+    fence_mbar_init();
+  }
+  cluster_sync();                              // every CTA's barriers are set up
   griddep_wait();
+  griddep_launch_dependents();
   const int4 tile = p.tiles[blockIdx.x / csize];
   if (tile.z <= 0) return;                     // the whole cluster leaves
   const int count = min(tile.z, kFewTile);
@@ -393,15 +487,13 @@ __global__ void __launch_bounds__(kFewThreads) requests_few_kernel(const FewArgs
   for (int t = 0; t < kFewTile; ++t) tok[t] = p.order[tile.y + min(t, count - 1)];
   const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
   // columns of U beyond the rank are zero
-  if (q == 0) {
-    for (int e = threadIdx.x; e < count * (p.width - ad.rank); e += kFewThreads) {
-      const int t = e / (p.width - ad.rank), r = ad.rank + e % (p.width - ad.rank);
-      int row = 0;
-#pragma unroll
-      for (int j = 0; j < kFewTile; ++j)
-        if (j == t) row = tok[j];
-      if (p.U) p.U[(int64_t)row * p.width + r] = 0.f;
-      if (p.sU) p.sU[(int64_t)row * p.width + r] = 0.f;
+  if (q == 0 && (p.U || p.sU)) {
+    const int rest = p.width - ad.rank;
+    for (int e = threadIdx.x; e < count * rest; e += kFewThreads) {
+      const int64_t row = p.order[tile.y + e / rest];
+      const int r = ad.rank + e % rest;
+      if (p.U) p.U[row * p.width + r] = 0.f;
+      if (p.sU) p.sU[row * p.width + r] = 0.f;
     }
   }
   if (ad.rank == 0) {
@@ -417,10 +509,27 @@ __global__ void __launch_bounds__(kFewThreads) requests_few_kernel(const FewArgs
     }
     return;
   }
-  if (count == 1) few_tile<1>(p, ad, tok, count, q, csize, s_part, s_u, s_red);
-  else if (count == 2) few_tile<2>(p, ad, tok, count, q, csize, s_part, s_u, s_red);
-  else if (count <= 4) few_tile<4>(p, ad, tok, count, q, csize, s_part, s_u, s_red);
-  else few_tile<8>(p, ad, tok, count, q, csize, s_part, s_u, s_red);
+  // shares of the columns: whole 16-byte words
+  const int kc = ((p.K / 8 + csize - 1) / csize) * 8, nc = ((p.N / 8 + csize - 1) / csize) * 8;
+  const int k0 = min(p.K, q * kc), k1 = min(p.K, k0 + kc);
+  const int n0 = min(p.N, q * nc), n1 = min(p.N, n0 + nc);
+  if (threadIdx.x >= 32 * kFewWarps) {
+    if ((threadIdx.x & 31) == 0) {
+      FewRing ring;
+      int issued = 0;
+      if (!few_produce(s, ring, issued, &w1, ad.first, ad.rank, k0, k1, false) ||
+          !few_produce(s, ring, issued, &w2, ad.first, ad.rank, n0, n1, true))
+        for (int i = 0; i < min(issued, kFewStages); ++i)        // let copies in flight land
+          mbar_wait_bounded(smem_u32(&s.full[i]), (uint32_t)((issued - 1 - i) / kFewStages & 1), nullptr);
+    }
+    __syncwarp();
+  } else {
+    if (count == 1) few_consume<1>(p, s, ad, tok, count, q, k0, k1, n0, n1);
+    else if (count == 2) few_consume<2>(p, s, ad, tok, count, q, k0, k1, n0, n1);
+    else if (count <= 4) few_consume<4>(p, s, ad, tok, count, q, k0, k1, n0, n1);
+    else few_consume<8>(p, s, ad, tok, count, q, k0, k1, n0, n1);
+  }
+  __syncwarp();
   cluster_sync();                              // no CTA leaves while its sums may still be read
 }
 
@@ -447,6 +556,7 @@ __global__ void __launch_bounds__(kFewGradThreads) requests_few_grads_kernel(con
   __shared__ __align__(16) float s_v[kFewGradTokens][16];
   __shared__ int s_tok[kFewGradTokens];
   griddep_wait();
+  griddep_launch_dependents();
   const int z = blockIdx.z;
   const int a = blockIdx.y / p.row_blocks, rb = blockIdx.y % p.row_blocks;
   const AdapterRows ad = adapter_rows(p.pool, a, p.width);
