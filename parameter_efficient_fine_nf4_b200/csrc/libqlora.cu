@@ -308,7 +308,7 @@ constexpr int kReqSmemMax = 226 * 1024;
 cudaError_t set_requests_attrs() {
   const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(requests_plan_kernel, at, (int)plan_smem_bytes(kReqMax, kReqMax));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_few_kernel, at, (int)sizeof(FewShared));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(requests_few_kernel, at, (int)few_smem_bytes(256, 4));
   if (e == cudaSuccess && cudaFuncSetAttribute(requests_few_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                               cudaSuccess)
     cudaGetLastError();                        // few_cluster16_fit then finds no such cluster
@@ -335,7 +335,7 @@ bool few_cluster16_fit() {
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(16);
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = sizeof(FewShared);
+  cfg.dynamicSmemBytes = few_smem_bytes(64, 16);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 16;

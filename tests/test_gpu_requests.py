@@ -17,10 +17,18 @@ CASES = {
     "smallest sizes": dict(k=8, d=8, ranks=[1], lens=[3], ids=[0]),
     "decoding": dict(k=256, d=512, ranks=[8, 16, 5, 64], lens=[1] * 19, ids=[i % 5 - 1 for i in range(19)]),
     "decoding, one adapter": dict(k=512, d=256, ranks=[16, 16], lens=[1] * 40, ids=[1] * 40),
+    "decoding, two blocks a tile": dict(k=1000, d=640, ranks=[24, 3], lens=[1] * 11, ids=[0, 1, 1, 0, 0, 0, 1, 1, 1, 1, -1]),
+    "decoding, wide": dict(k=4104, d=1032, ranks=[64, 12, 33], lens=[1, 2, 3, 1, 5, 1, 8], ids=[0, 1, 2, 0, 1, -1, 2]),
+    "decoding, wide output": dict(k=264, d=8192, ranks=[16, 40], lens=[2, 1, 4, 9], ids=[1, 0, 0, 1]),
+    "one token, wide": dict(k=8192, d=4096, ranks=[48], lens=[1], ids=[0]),
+    "few tokens, rank 256": dict(k=2048, d=2056, ranks=[256, 100], lens=[3, 9, 1], ids=[0, 1, 0]),
+    "few tokens, rank 128": dict(k=4096, d=512, ranks=[128], lens=[2], ids=[0]),
+    "the most few tokens": dict(k=520, d=4096, ranks=[20, 9], lens=[100, 28], ids=[1, 0]),
     "padded batch": dict(k=256, d=264, ranks=[12, 4], lens=[3, 0, 5, -2, 1], ids=[1, 0, 0, 1, 9], T=21),
     "cut batch": dict(k=136, d=72, ranks=[3, 30], lens=[9, 30, 2000000000, 2000000000], ids=[0, 1, 0, 1], T=70),
     "empty requests only": dict(k=64, d=64, ranks=[8], lens=[0, 0], ids=[0, 0], T=5),
     "no requests": dict(k=64, d=64, ranks=[8], lens=[], ids=[], T=5),
+    "one more than few tokens": dict(k=520, d=512, ranks=[20, 9], lens=[100, 29], ids=[1, 0]),
     "tiles end inside": dict(k=320, d=192, ranks=[16, 40, 7], lens=[127, 1, 128, 129, 8, 7, 9],
                              ids=[0, 1, 1, 2, 0, 2, 1]),
     "rank 256": dict(k=200, d=328, ranks=[256, 17], lens=[70, 65, 30], ids=[0, 1, 0]),
