@@ -363,10 +363,21 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
   const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
   if (ad.rank == 0) {
     if (p.out != p.base) {
+      // the base's rows as they are, eight 16-byte words of a thread in flight
       const int n8 = (n1 - n0) / 8;
-      for (int e = threadIdx.x; e < count * n8; e += kReqThreads) {
-        const int64_t at = (int64_t)p.order[tile.y + e / n8] * p.N + n0 + (e % n8) * 8;
-        *reinterpret_cast<uint4*>(p.out + at) = p.base ? *reinterpret_cast<const uint4*>(p.base + at) : make_uint4(0, 0, 0, 0);
+      for (int e0 = threadIdx.x; e0 < count * n8; e0 += 8 * kReqThreads) {
+        uint4 v[8];
+        int64_t at[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = min(e0 + i * kReqThreads, count * n8 - 1);
+          at[i] = (int64_t)p.order[tile.y + e / n8] * p.N + n0 + (e % n8) * 8;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p.base ? *reinterpret_cast<const uint4*>(p.base + at[i]) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e0 + i * kReqThreads < count * n8) *reinterpret_cast<uint4*>(p.out + at[i]) = v[i];
       }
     }
     return;
