@@ -63,14 +63,20 @@ struct RowLane {
   int tok[4];
   bool whole;
 };
-__device__ __forceinline__ RowLane row_lane(const int32_t* order, int first, int count, int i) {
-  RowLane r;
+__device__ __forceinline__ void row_tokens(RowLane& r, const int32_t* order, int first, int count, int i) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) r.tok[j] = order[first + max(0, min(4 * i + j, count - 1))];
+}
+__device__ __forceinline__ void row_whole(RowLane& r, int count, int i) {
   const int lane = threadIdx.x & 31;
   const int a = __shfl_sync(0xFFFFFFFFu, r.tok[0], lane & ~7);
   const int b = __shfl_sync(0xFFFFFFFFu, r.tok[3], lane | 7);
   r.whole = (i / 8 + 1) * 32 <= count && b - a == 31;
+}
+__device__ __forceinline__ RowLane row_lane(const int32_t* order, int first, int count, int i) {
+  RowLane r;
+  row_tokens(r, order, first, count, i);
+  row_whole(r, count, i);
   return r;
 }
 // This lane's part of one 64-column block of token rows (rounded up to 16).
@@ -221,6 +227,7 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_bf16_f32(128, r16, 0, 0);
+    const uint64_t a0 = smem_desc_sw128(sbase, 16, 1024), b0 = smem_desc_sw128(sbase + kReqRows, 16, 1024);
     bool ok = true;
     int last = -1;
     for (int s = 0; s < steps && ok; ++s) {
@@ -229,8 +236,8 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
            mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
-      const uint64_t a = smem_desc_sw128(st, 16, 1024), b = smem_desc_sw128(st + kReqRows, 16, 1024);
+      const uint32_t off = (uint32_t)(ring.at * p.stage_bytes) >> 4;
+      const uint64_t a = a0 + off, b = b0 + off;
 #pragma unroll
       for (int j = 0; j < 4; ++j) umma_bf16(tmem + (uint32_t)(buf * r16), a + 2u * j, b + 2u * j, idesc, j ? 1u : 0u);
       last = s;
@@ -450,6 +457,7 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_bf16_f32(128, 64, 0, 1);
+    const uint64_t v0 = smem_desc_sw128(sbase, 16, 1024), w0 = smem_desc_sw128(stage0 + kReqRows, 8192, 1024);
     bool ok = mbar_wait_bounded(v_bar, 0, abort_flag);
     int any = 0, last = 0;
     for (int s = 0; s < chunks && ok; ++s) {
@@ -459,18 +467,19 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(buf * 64);
-      const uint32_t w = stage0 + (uint32_t)(ring.at * p.stage_bytes) + kReqRows;
+      const uint64_t w = w0 + ((uint32_t)(ring.at * p.stage_bytes) >> 4);
       uint32_t acc = 0;
       for (int c = 0; c < r16; c += 64) {
-        const int rc = min(64, r16 - c);
-        const uint32_t vb = sbase + (uint32_t)(c / 64 * 2 * kReqRows);
-        for (int k = 0; k < 2 * rc; k += 16) {          // hi, then mid
-          const int kk = k < rc ? k : k - rc, wr = c + kk;
-          const uint64_t a = smem_desc_sw128(vb + (uint32_t)((k < rc ? 0 : kReqRows) + kk * 2), 16, 1024);
-          const uint64_t b = smem_desc_sw128(w + (uint32_t)wr * 128u, 8192, 1024);
-          umma_bf16(d, a, b, idesc, acc);
-          acc = 1;
-        }
+        const int ks = min(64, r16 - c) / 16;
+        // hi, then mid (a box further); 16 of the rank are 32 bytes of V's rows and 16 rows of the factor
+        const uint64_t v = v0 + (uint64_t)(c / 64 * (2 * kReqRows / 16)), wc = w + (uint64_t)(c * 8);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < ks) {
+            umma_bf16(d, v + (uint64_t)(2 * k), wc + (uint64_t)(128 * k), idesc, acc);
+            acc = 1;
+            umma_bf16(d, v + (uint64_t)(kReqRows / 16 + 2 * k), wc + (uint64_t)(128 * k), idesc, 1u);
+          }
       }
       any = 1;
       last = buf;
@@ -544,54 +553,124 @@ struct GradArgs {
   PoolArgs pool;
   int cols[2], blocks[2];       // columns of the two factors, and their blocks of 256
   float* dW[2];
-  int width, chunks, csize, stages, stage_bytes, tmem_cols;
+  float* part;                  // [CTA][2][64 or width][256]: sums of units that CTAs share
+  int4* cut;                    // [CTA]: {factor, row, column, rank | CTAs that go on << 16} of its last unit, if that is cut
+  int width, stages, stage_bytes, tmem_cols;
 };
 constexpr int kGradCols = 256;
+constexpr int kReqGradThreads = 320;            // warps 2-9: epilogue, one per 128 columns and quarter of their rows
 
-// One adapter, 64 of its rank, 256 columns: D[column][hi | mid | lo] sums over
-// the adapter's tokens (A operand: token rows, MN-major; B operand: V,
-// MN-major), the CTAs of a cluster taking every csize-th 64 tokens; the three
-// parts and the CTAs' sums are added in a fixed order.  Only the hi part is
-// moved to registers stage by stage: mid and lo are 2^-8 of it and may be cut
-// 2^8 times as often.
+// A unit is one adapter, 64 of its rank and 256 columns of one factor; its work
+// is one step per 64 tokens (an adapter without tokens: one step that only
+// writes zeros).  The steps of all units, unit by unit, are cut into equal
+// parts, one per CTA, whatever the adapters' lengths are.  A CTA that has all
+// steps of a unit writes its gradient; the sums of a unit that is cut go to
+// the workspace (slot 0: the unit began in an earlier CTA, slot 1: it goes on in
+// a later one), and requests_grads_join_kernel adds them in order.
+struct GradUnit {
+  int a, unit, units;           // adapter; block + per * (64 of the rank); how many it has
+  int steps, lo, cnt;           // steps of a unit; the adapter's tokens in `order`
+  AdapterRows ad;
+};
+__device__ __forceinline__ int grad_per(const GradArgs& p) { return p.blocks[0] + p.blocks[1]; }
+__device__ __forceinline__ void grad_adapter(const GradArgs& p, GradUnit& g, int a) {
+  g.a = a;
+  g.ad = adapter_rows(p.pool, a, p.width);
+  g.lo = p.seg[a];
+  g.cnt = p.seg[a + 1] - g.lo;
+  g.units = (g.ad.rank + 63) / 64 * grad_per(p);
+  g.steps = max(1, (g.cnt + 63) / 64);
+}
+__device__ __forceinline__ void grad_next_unit(const GradArgs& p, GradUnit& g) {
+  if (++g.unit < g.units) return;
+  g.unit = 0;
+  int a = g.a;
+  do grad_adapter(p, g, ++a);
+  while (g.units == 0);         // never past the last: the caller knows that steps are left
+}
+// Where part `part` of the steps begins: step `at` of all `total`, in adapter a,
+// whose first step is `base`.  As many parts as there are CTAs, or steps if
+// these are fewer.  The whole block calls it.
+struct GradScan {
+  long long warp[32];
+  long long at, base, total;
+  int a, parts;
+};
+__device__ __forceinline__ void grad_locate(const GradArgs& p, GradScan& s, int part, int parts) {
+  const int per = (p.pool.n + blockDim.x - 1) / blockDim.x;
+  const int a0 = min(p.pool.n, (int)threadIdx.x * per), a1 = min(p.pool.n, a0 + per);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sum = 0;
+  for (int a = a0; a < a1; ++a) {
+    GradUnit g;
+    grad_adapter(p, g, a);
+    sum += (long long)g.units * g.steps;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) s.warp[warp] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+    if (w < warp) before += s.warp[w];
+    total += s.warp[w];
+  }
+  long long base = before + inc - sum;
+  parts = (int)min((long long)parts, max(1ll, total));
+  const long long at = part < parts ? total * part / parts : total;
+  if (at >= base && at < base + sum) {
+    for (int a = a0; a < a1; ++a) {
+      GradUnit g;
+      grad_adapter(p, g, a);
+      const long long w = (long long)g.units * g.steps;
+      if (at < base + w) {
+        s.a = a;
+        s.base = base;
+        break;
+      }
+      base += w;
+    }
+  }
+  if (threadIdx.x == 0) {
+    s.at = at;
+    s.total = total;
+    s.parts = parts;
+  }
+  __syncthreads();
+}
+struct GradPlace {
+  int z, c0, cols, rc0, rc;
+};
+__device__ __forceinline__ GradPlace grad_place(const GradArgs& p, const GradUnit& g) {
+  GradPlace w;
+  const int per = grad_per(p), block = g.unit % per;
+  w.rc0 = g.unit / per * 64;
+  w.z = block >= p.blocks[0] ? 1 : 0;
+  w.cols = w.z ? p.cols[1] : p.cols[0];
+  w.c0 = (w.z ? block - p.blocks[0] : block) * kGradCols;
+  w.rc = min(64, ((g.ad.rank + 15) & ~15) - w.rc0);
+  return w;
+}
+
+// D[column][hi | mid | lo] (A operand: token rows, MN-major; B operand: V,
+// MN-major).  Only the hi part is moved to registers step by step: mid and lo
+// are 2^-8 of it and may be cut 2^8 times as often.
 template <int NI>                                // 16 of the rank each: 1 or 4
-__global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_kernel(
+__global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_grads_kernel(
     const __grid_constant__ CUtensorMap box0, const __grid_constant__ CUtensorMap row0, const __grid_constant__ CUtensorMap terms0,
     const __grid_constant__ CUtensorMap box1, const __grid_constant__ CUtensorMap row1, const __grid_constant__ CUtensorMap terms1,
     const __grid_constant__ GradArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 4];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ GradScan s_scan;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = (int)(blockIdx.x % p.csize);
-  int unit = (int)(blockIdx.x / p.csize);
-  const int per = p.blocks[0] + p.blocks[1];
-  const int block = unit % per;
-  unit /= per;
-  const int rc0 = (unit % p.chunks) * 64;
-  const int a = unit / p.chunks;
-  const int z = block >= p.blocks[0] ? 1 : 0;
-  const int cols = z ? p.cols[1] : p.cols[0];
-  const int c0 = (z ? block - p.blocks[0] : block) * kGradCols;
-  griddep_wait();
-  griddep_launch_dependents();
-  const AdapterRows ad = adapter_rows(p.pool, a, p.width);
-  if (rc0 >= ad.rank) return;                    // the whole cluster
-  const int rc = min(64, ((ad.rank + 15) & ~15) - rc0);
-  const int lo = p.seg[a], cnt = p.seg[a + 1] - lo;
-  const int vrow0 = p.tile_first[a] * kReqTile;
-  const int all = (cnt + 63) / 64;
-  const int steps = all > q ? (all - q + p.csize - 1) / p.csize : 0;
-  const CUtensorMap* box = z ? &box1 : &box0;
-  const CUtensorMap* rowm = z ? &row1 : &row0;
-  const CUtensorMap* terms = z ? &terms1 : &terms0;
-  float* dW = z ? p.dW[1] : p.dW[0];
-  const int halves = cols - c0 > 128 ? 2 : 1;    // 128-column MMAs in use
-  const int blocks64 = min(4, (cols - c0 + 63) / 64);   // (an unloaded last block is never stored)
-  const int vboxes = 1 + (2 * rc + 63) / 64;
   volatile int* abort_flag = &s_abort;
 
   Ring ring;
@@ -599,6 +678,7 @@ __global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_k
   ring.empty = smem_u32(&s_bar[8]);
   ring.stages = p.stages;
   const uint32_t acc_full = smem_u32(&s_bar[16]), acc_empty = smem_u32(&s_bar[18]);   // two each
+  const uint32_t rest_empty = smem_u32(&s_bar[20]);
   // Tensor Memory: hi of each half in two alternating sets, then mid | lo of each half
   const uint32_t rcw = (uint32_t)min(64, p.width);
   if (threadIdx.x == 0) {
@@ -608,11 +688,20 @@ __global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_k
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8u * i, 1);
-      mbar_init(acc_empty + 8u * i, 4);
+      mbar_init(acc_empty + 8u * i, 8);
     }
+    mbar_init(rest_empty, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
+  griddep_wait();
+  griddep_launch_dependents();
+  grad_locate(p, s_scan, (int)blockIdx.x, (int)gridDim.x);
+  const long long at = s_scan.at, total = s_scan.total;
+  const int parts = s_scan.parts;
+  const long long left0 = (int)blockIdx.x < parts ? total * (blockIdx.x + 1) / parts - at : 0;
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (left0 <= 0) return;
   if (warp == 1) {
     tmem_alloc(smem_u32(&s_tmem), (uint32_t)p.tmem_cols);
     tmem_relinquish();
@@ -621,27 +710,49 @@ __global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_k
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  GradUnit g;
+  grad_adapter(p, g, s_scan.a);
+  g.unit = (int)((at - s_scan.base) / g.steps);
+  int step0 = (int)((at - s_scan.base) % g.steps);
+  long long left = left0;
 
   if (warp == 0) {
     const int i = lane & 15;                     // four token rows of 64
-    int issued = 0;
-    for (int s = 0; s < steps; ++s) {
-      const int first = (q + s * p.csize) * 64;
-      const int m = min(64, cnt - first);
-      const RowLane r = row_lane(p.order, lo + first, m, i);
-      int ok = 1;
-      if (lane == 0) {
-        ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
-        if (ok) mbar_arrive_expect_tx(ring.full_bar(), row_bytes(m) * blocks64 + (uint32_t)vboxes * 8192u);
+    int issued = 0, ok = 1;
+    while (left > 0 && ok) {
+      const GradPlace w = grad_place(p, g);
+      const int step1 = (int)min((long long)g.steps, step0 + left);
+      const CUtensorMap* box = w.z ? &box1 : &box0;
+      const CUtensorMap* rowm = w.z ? &row1 : &row0;
+      const CUtensorMap* terms = w.z ? &terms1 : &terms0;
+      const int blocks64 = min(4, (w.cols - w.c0 + 63) / 64);       // (an unloaded last block is never stored)
+      const int vboxes = 1 + (2 * w.rc + 63) / 64;
+      const int vrow0 = p.tile_first[g.a] * kReqTile;
+      RowLane ahead;                             // the next step's tokens, on their way while this one waits
+      if (g.cnt > 0) row_tokens(ahead, p.order, g.lo + step0 * 64, min(64, g.cnt - step0 * 64), i);
+      for (int s = step0; s < step1 && g.cnt > 0; ++s) {
+        const int first = s * 64;
+        const int m = min(64, g.cnt - first);
+        RowLane r = ahead;
+        if (s + 1 < step1) row_tokens(ahead, p.order, g.lo + first + 64, min(64, g.cnt - first - 64), i);
+        row_whole(r, m, i);
+        if (lane == 0) {
+          ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
+          if (ok) mbar_arrive_expect_tx(ring.full_bar(), row_bytes(m) * blocks64 + (uint32_t)vboxes * 8192u);
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
+        for (int c = lane >> 4; c < blocks64; c += 2)
+          load_rows(st + (uint32_t)c * 8192u, box, rowm, ring.full_bar(), w.c0 + c * 64, r, i, m);
+        if (lane < vboxes)
+          tma_load_2d(st + 4u * 8192u + (uint32_t)lane * 8192u, terms, ring.full_bar(), w.rc0 * 3 + 64 * lane, vrow0 + first);
+        ring.next();
+        ++issued;
       }
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
-      for (int c = lane >> 4; c < blocks64; c += 2)
-        load_rows(st + (uint32_t)c * 8192u, box, rowm, ring.full_bar(), c0 + c * 64, r, i, m);
-      if (lane < vboxes)
-        tma_load_2d(st + 4u * 8192u + (uint32_t)lane * 8192u, terms, ring.full_bar(), rc0 * 3 + 64 * lane, vrow0 + first);
-      ring.next();
-      ++issued;
+      left -= step1 - step0;
+      step0 = 0;
+      if (left > 0) grad_next_unit(p, g);
     }
     if (*abort_flag && lane == 0) {
       for (int k = 0; k < min(issued, p.stages); ++k) {
@@ -650,117 +761,165 @@ __global__ void __launch_bounds__(kReqThreads, NI == 1 ? 2 : 1) requests_grads_k
       }
     }
   } else if (warp == 1 && lane == 0) {
-    const uint32_t id_hi = idesc_bf16_f32(128, rc, 1, 1), id_rest = idesc_bf16_f32(128, 2 * rc, 1, 1);
+    // descriptors of stage 0: one thread issues, so an address costs it an addition
+    const uint64_t xd0 = smem_desc_sw128(sbase, 8192, 1024), vd0 = smem_desc_sw128(sbase + 4u * 8192u, 8192, 1024);
     bool ok = true;
-    int last = -1;
-    for (int s = 0; s < steps && ok; ++s) {
-      const int buf = s & 1;
-      ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((s >> 1) & 1) ^ 1), abort_flag) &&
-           mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const int m = min(64, cnt - (q + s * p.csize) * 64);
-      const uint32_t st = sbase + (uint32_t)(ring.at * p.stage_bytes);
-      const uint32_t v = st + 4u * 8192u;
-      for (int h = 0; h < halves; ++h) {
-        const uint32_t hi = tmem + (uint32_t)(buf * 2 + h) * rcw, rest = tmem + 4u * rcw + (uint32_t)h * 2u * rcw;
-        for (int k = 0; k < (m + 15) / 16; ++k) {
-          const uint64_t xd = smem_desc_sw128(st + (uint32_t)(h * 16384 + k * 2048), 8192, 1024);
-          umma_bf16(hi, xd, smem_desc_sw128(v + (uint32_t)k * 2048u, 8192, 1024), id_hi, k ? 1u : 0u);
-          umma_bf16(rest, xd, smem_desc_sw128(v + 8192u + (uint32_t)k * 2048u, 8192, 1024), id_rest, (s | k) ? 1u : 0u);
-        }
+    int n = 0, pieces = 0;                       // steps and pieces of units so far
+    while (left > 0 && ok) {
+      const GradPlace w = grad_place(p, g);
+      const int step1 = (int)min((long long)g.steps, step0 + left);
+      const int halves = w.cols - w.c0 > 128 ? 2 : 1;               // 128-column MMAs in use
+      const uint32_t id_hi = idesc_bf16_f32(128, w.rc, 1, 1), id_rest = idesc_bf16_f32(128, 2 * w.rc, 1, 1);
+      if (g.cnt > 0) {
+        // mid | lo of the last piece have been read
+        ok = mbar_wait_bounded(rest_empty, (uint32_t)((pieces & 1) ^ 1), abort_flag);
+        ++pieces;
       }
-      last = s;
-      umma_commit(ring.empty_bar());
-      umma_commit(acc_full + 8u * buf);
-      ring.next();
-    }
-    if (!ok && last >= 0) mbar_wait_bounded(acc_full + 8u * (last & 1), (uint32_t)((last >> 1) & 1), nullptr);
-  }
-  __syncwarp();
-
-  // [rank][column] sums of this CTA in shared memory
-  float* s_part = reinterpret_cast<float*>(smem);
-  if (warp >= 2) {
-    const int quarter = warp & 3;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    float acc[2][NI][16];
+      for (int s = step0; s < step1 && g.cnt > 0 && ok; ++s, ++n) {
+        const int buf = n & 1;
+        ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag) &&
+             mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int m = min(64, g.cnt - s * 64);
+        const uint32_t off = (uint32_t)(ring.at * p.stage_bytes) >> 4;
+        const uint64_t xd = xd0 + off, vd = vd0 + off;
+        const uint32_t more = s > step0 ? 1u : 0u;
+        const int ks = (m + 15) / 16;
+        for (int h = 0; h < halves; ++h) {
+          const uint32_t hi = tmem + (uint32_t)(buf * 2 + h) * rcw, rest = tmem + 4u * rcw + (uint32_t)h * 2u * rcw;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+          for (int k = 0; k < 4; ++k)
+            if (k < ks) {
+              umma_bf16(hi, xd + (uint64_t)(h * 1024 + k * 128), vd + (uint64_t)(k * 128), id_hi, k ? 1u : 0u);
+              umma_bf16(rest, xd + (uint64_t)(h * 1024 + k * 128), vd + (uint64_t)(512 + k * 128), id_rest, k ? 1u : more);
+            }
+        }
+        umma_commit(ring.empty_bar());
+        umma_commit(acc_full + 8u * buf);
+        ring.next();
+      }
+      left -= step1 - step0;
+      step0 = 0;
+      if (left > 0 && ok) grad_next_unit(p, g);
+    }
+    if (!ok && n > 0) mbar_wait_bounded(acc_full + 8u * ((n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), nullptr);
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, h = (warp - 2) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    bool ok = true;
+    int n = 0;
+    while (left > 0 && ok) {
+      const GradPlace w = grad_place(p, g);
+      const int step1 = (int)min((long long)g.steps, step0 + left);
+      const bool mine = h * 128 < w.cols - w.c0;
+      float acc[NI][16];
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[h][i][j] = 0.f;
-    bool ok = true;
-    for (int s = 0; s <= steps && steps > 0; ++s) {
-      // the stages' hi products, and behind the last one mid | lo
-      const bool rest = s == steps;
-      const int buf = s & 1;
-      if (!rest) {
-        ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag);
+        for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+      for (int s = step0; s < step1 && g.cnt > 0; ++s, ++n) {
+        const int buf = n & 1;
+        ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((n >> 1) & 1), abort_flag);
         __syncwarp();
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc_fence_after();
-      }
+        if (mine) {
+          uint32_t v[NI][16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h >= halves) break;
+          for (int i = 0; i < NI; ++i)
+            if (16 * i < w.rc) tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * i, v[i]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (16 * i >= rc) break;
-          uint32_t v[16];
-          if (!rest) {
-            tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * i, v);
-            tmem_ld_wait();
-          } else {
-            uint32_t w[16];
-            const uint32_t at = lanes + 4u * rcw + (uint32_t)h * 2u * rcw + 16u * i;
-            tmem_ld_32x32b_x16(at, v);
-            tmem_ld_32x32b_x16(at + (uint32_t)rc, w);
-            tmem_ld_wait();
+          for (int i = 0; i < NI; ++i)
+            if (16 * i < w.rc)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[h][i][j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[i][j]);
         }
-      }
-      if (!rest) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
       }
+      if (g.cnt > 0 && ok) {
+        // mid | lo: the last step's barrier covers them
+        if (mine) {
+          const uint32_t t = lanes + 4u * rcw + (uint32_t)h * 2u * rcw;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            if (16 * i >= w.rc) break;
+            uint32_t v[16], x[16];
+            tmem_ld_32x32b_x16(t + 16u * i, v);
+            tmem_ld_32x32b_x16(t + (uint32_t)w.rc + 16u * i, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[j]) + __uint_as_float(x[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rest_empty);
+      }
+      if (ok) {
+        const bool whole = step0 == 0 && step1 == g.steps;
+        float* out;
+        int64_t ld;
+        if (whole) {
+          ld = w.cols;
+          out = (w.z ? p.dW[1] : p.dW[0]) + (int64_t)(g.ad.first + w.rc0) * ld + w.c0;
+        } else {
+          ld = kGradCols;
+          out = p.part + ((int64_t)blockIdx.x * 2 + (step0 > 0 ? 0 : 1)) * (int64_t)rcw * kGradCols;
+          if (step0 == 0 && warp == 2 && lane == 0) {
+            // the CTAs behind this one that have a part of the unit
+            const long long end = total * (blockIdx.x + 1) / parts + g.steps - step1;
+            int more = 0;
+            for (int k = blockIdx.x + 1; k < parts && total * k / parts < end; ++k) ++more;
+            p.cut[blockIdx.x] = make_int4(w.z, g.ad.first + w.rc0, w.c0, w.rc | more << 16);
+          }
+        }
+        const int c = h * 128 + quarter * 32 + lane;
+        if (w.c0 + c < w.cols)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+            if (16 * i < w.rc)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) out[(int64_t)(16 * i + j) * ld + c] = acc[i][j];
+      }
+      left -= step1 - step0;
+      step0 = 0;
+      if (left > 0 && ok) grad_next_unit(p, g);
     }
     tc_fence_before();
-    named_bar_sync(1, 128);                      // the sums lie over the stages
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (h < halves && 16 * i < rc)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            s_part[(16 * i + j) * kGradCols + h * 128 + quarter * 32 + lane] = acc[h][i][j];
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
-  if (p.csize > 1) cluster_sync();
-  const uint32_t part = smem_u32(s_part);
-  const int per_cta = (rc * (kGradCols / 4) + p.csize - 1) / p.csize;
-  const int e1 = min(rc * (kGradCols / 4), (q + 1) * per_cta);
-  for (int e = q * per_cta + threadIdx.x; e < e1; e += kReqThreads) {
-    const int j = e / (kGradCols / 4), c = (e % (kGradCols / 4)) * 4;
-    if (c0 + c >= cols) continue;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const uint32_t at = part + (uint32_t)(j * kGradCols + c) * 4u;
-    for (int k = 0; k < p.csize; ++k) {
-      const float4 f = p.csize > 1 ? ld_shared_cluster_f4(mapa_shared(at, (uint32_t)k))
-                                   : *reinterpret_cast<const float4*>(s_part + j * kGradCols + c);
+}
+
+// Adds the parts of the unit that CTA blockIdx.x began and others went on with;
+// blockIdx.y takes a quarter of the rows.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) requests_grads_join_kernel(const GradArgs p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int4 cut = p.cut[blockIdx.x];
+  const int rc = cut.w & 0xFFFF, more = cut.w >> 16;
+  if (rc == 0) return;
+  const int cols = cut.x ? p.cols[1] : p.cols[0];
+  const int64_t slot = (int64_t)min(64, p.width) * kGradCols;
+  float* out = (cut.x ? p.dW[1] : p.dW[0]) + (int64_t)cut.y * cols + cut.z;
+  const int rows = rc / 4;
+  for (int e = threadIdx.x; e < rows * (kGradCols / 4); e += kJoinThreads) {
+    const int j = blockIdx.y * rows + e / (kGradCols / 4), c = (e % (kGradCols / 4)) * 4;
+    if (cut.z + c >= cols) continue;
+    const float* in = p.part + (int64_t)blockIdx.x * 2 * slot + (int64_t)j * kGradCols + c;
+    float4 v = *reinterpret_cast<const float4*>(in + slot);
+    for (int k = 1; k <= more; ++k) {
+      const float4 f = *reinterpret_cast<const float4*>(in + (int64_t)k * 2 * slot);
       v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
     }
-    *reinterpret_cast<float4*>(dW + (int64_t)(ad.first + rc0 + j) * cols + c0 + c) = v;
+    *reinterpret_cast<float4*>(out + (int64_t)j * cols + c) = v;
   }
-  if (p.csize > 1) cluster_sync();
 }
 
 }  // namespace qlora
