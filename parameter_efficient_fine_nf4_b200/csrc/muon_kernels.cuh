@@ -211,14 +211,18 @@ __global__ void __launch_bounds__(kGram64Threads) muon_gram64_kernel(const MuonA
 // R0 from the partials, then `steps` rounds of the quintic's polynomial, all in
 // shared memory: a cluster of NB CTAs, each with 8 rows.  Q R needs R whole and
 // the CTA's own rows of Q, then R Q R and P Q need Q whole, so Q and R are
-// exchanged once each per round (every CTA writes its rows into every other's
-// copy); a product of 8 rows is one 8 x 8 block per warp.  Bound by the
-// latency of these exchanges.
+// exchanged once each per round: every CTA stores its rows asynchronously into
+// every other's copy, counted on the receiver's barrier (0.9 us less an
+// exchange than plain stores and a cluster barrier).  Both are kept twice, by
+// round: a CTA that runs ahead writes the next round's copy, and it gets no
+// further without this CTA's rows, which leave after its last read of the old
+// ones.  A product of 8 rows is one 8 x 8 block per warp; four of them a round
+// are about half of the time, the exchanges the rest.
 template <int NB>
 struct Poly64 {
   static constexpr int kRp = 8 * NB, kPitch = kRp + 4;     // pitch of 4 mod 16: fragments without bank conflicts
   static constexpr int kThreads = 32 * NB;
-  static constexpr int kSmem = (2 * kRp + 4 * 8) * kPitch * 8;
+  static constexpr int kSmem = (4 * kRp + 3 * 8) * kPitch * 8;
 };
 template <int NB>
 __device__ __forceinline__ void poly_product(double (&d)[2], const double* rows, const double* sym) {
@@ -233,29 +237,49 @@ __device__ __forceinline__ void poly_product(double (&d)[2], const double* rows,
   d[0] += e[0];
   d[1] += e[1];
 }
+// Two doubles into the same place of every CTA of the cluster: this one's by a
+// plain store, the others' counted on their barrier.
 template <int NB>
-__device__ __forceinline__ void poly_spread(const double* at, const double (&d)[2]) {
+__device__ __forceinline__ void poly_spread(double* at, const double (&d)[2], int q, uint32_t bar) {
+  *reinterpret_cast<double2*>(at) = make_double2(d[0], d[1]);
   const uint32_t a = smem_u32(at);
+  const int2 x = make_int2(__double2loint(d[0]), __double2hiint(d[0])), y = make_int2(__double2loint(d[1]), __double2hiint(d[1]));
 #pragma unroll
-  for (int c = 0; c < NB; ++c)
-    asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(mapa_shared(a, (uint32_t)c)), "d"(d[0]), "d"(d[1]) : "memory");
+  for (int c = 1; c < NB; ++c) {
+    const uint32_t to = (uint32_t)((q + c) % NB);
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     mapa_shared(a, to)),
+                 "r"(x.x), "r"(x.y), "r"(y.x), "r"(y.y), "r"(mapa_shared(bar, to))
+                 : "memory");
+  }
 }
 template <int NB, bool kTall>
 __global__ void __launch_bounds__(Poly64<NB>::kThreads) muon_poly64_kernel(const MuonArgs p, int parts, int steps) {
   using C = Poly64<NB>;
-  constexpr int kTiles = Gram64<NB>::kTiles;
+  constexpr int kTiles = Gram64<NB>::kTiles, kMat = C::kRp * C::kPitch;
+  constexpr uint32_t kOthers = (NB - 1) * 8 * C::kRp * 8;  // bytes that the other CTAs send per exchange
   extern __shared__ __align__(16) double s_mat[];
-  double* R = s_mat;                               // [rp][pitch]
-  double* Q = R + C::kRp * C::kPitch;
-  double* H = Q + C::kRp * C::kPitch;              // 8 rows
+  double* H = s_mat + 4 * kMat;                    // 8 rows; R and Q of two rounds before it
   double* P[2] = {H + 8 * C::kPitch, H + 16 * C::kPitch};
   __shared__ double s_inv;
+  __shared__ __align__(8) uint64_t s_bar[2];       // Q, R
+  __shared__ int s_abort;
+  const uint32_t q_bar = smem_u32(&s_bar[0]), r_bar = smem_u32(&s_bar[1]);
+  if (threadIdx.x == 0) {
+    mbar_init(q_bar, 1);
+    mbar_init(r_bar, 1);
+    s_abort = 0;
+    fence_mbar_init();
+    mbar_arrive_expect_tx(q_bar, kOthers);
+    mbar_arrive_expect_tx(r_bar, kOthers);
+  }
+  __syncthreads();
+  cluster_sync();                                  // every CTA runs before its memory is written
   griddep_wait();
   griddep_launch_dependents();
   const int q = (int)cluster_ctarank();
   const int64_t mat = blockIdx.x / NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
-  cluster_sync();                                  // every CTA runs before its memory is written
   // this CTA's 8 rows of the Gram matrix: the sum of the partials
   const double* part = p.part + mat * parts * (int64_t)(kTiles * 64);
   for (int e = threadIdx.x; e < 8 * C::kRp; e += C::kThreads) {
@@ -266,72 +290,79 @@ __global__ void __launch_bounds__(Poly64<NB>::kThreads) muon_poly64_kernel(const
     const int x = up ? bi : bj, y = up ? bj : bi;
     const int at = (x * NB - x * (x - 1) / 2 + y - x) * 64 + (up ? ri * 8 + rj : rj * 8 + ri);
     double v = 0.0;
+#pragma unroll 8
     for (int k = 0; k < parts; ++k) v += part[k * kTiles * 64 + at];
-    const uint32_t to = smem_u32(R + i * C::kPitch + j);
+    const uint32_t to = smem_u32(s_mat + i * C::kPitch + j);
 #pragma unroll
     for (int c = 0; c < NB; ++c)
       asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(to, (uint32_t)c)), "d"(v) : "memory");
   }
+  __syncwarp();
   cluster_sync();
   if (warp == 0) {
     double t = 0.0;
-    for (int i = lane; i < C::kRp; i += 32) t += R[i * C::kPitch + i];
+    for (int i = lane; i < C::kRp; i += 32) t += s_mat[i * C::kPitch + i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     if (lane == 0) s_inv = 1.0 / (sqrt(t) + p.eps);
   }
   __syncthreads();
   const double inv = s_inv;
-  for (int e = threadIdx.x; e < C::kRp * C::kRp; e += C::kThreads) R[e / C::kRp * C::kPitch + e % C::kRp] *= inv * inv;
+  for (int e = threadIdx.x; e < C::kRp * C::kRp; e += C::kThreads) s_mat[e / C::kRp * C::kPitch + e % C::kRp] *= inv * inv;
   __syncthreads();
 
   // fragment addresses: this CTA's rows of R, Q; a warp's 8 columns (rows of a symmetric matrix)
-  const int mine = (8 * q + hi) * C::kPitch, col = (8 * warp + hi) * C::kPitch;
+  const int mine = (8 * q + hi) * C::kPitch + lo, col = (8 * warp + hi) * C::kPitch + lo, own = hi * C::kPitch + lo;
   const int out = hi * C::kPitch + 8 * warp + 2 * lo, at = 8 * q * C::kPitch + out;
   int cur = 0;
   for (int it = 0; it < steps; ++it) {
     const bool last = it == steps - 1;
-    double d[2];
-    poly_product<NB>(d, R + mine + lo, R + col + lo);
+    double* R = s_mat + (it & 1) * kMat;
+    double* Q = s_mat + (2 + (it & 1)) * kMat;
+    double d[2], e[2];
+    poly_product<NB>(d, R + mine, R + col);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      d[e] = p.c * d[e] + p.b * R[at + e];
-      if (8 * q + hi == 8 * warp + 2 * lo + e) d[e] += p.a;
+    for (int i = 0; i < 2; ++i) {
+      d[i] = p.c * d[i] + p.b * R[at + i];
+      if (8 * q + hi == 8 * warp + 2 * lo + i) d[i] += p.a;
     }
-    poly_spread<NB>(Q + at, d);
-    if (it == 0) {                                 // P = Q; it carries the norm of x0 = u inv
-      P[0][out] = inv * d[0];
-      P[0][out + 1] = inv * d[1];
-    }
+    poly_spread<NB>(Q + at, d, q, q_bar);
+    if (it == 0) *reinterpret_cast<double2*>(P[0] + out) = make_double2(inv * d[0], inv * d[1]);   // with the norm of x0 = u inv
     if (!last) {
       __syncthreads();                             // this CTA's rows of Q
-      poly_product<NB>(d, Q + mine + lo, R + col + lo);
-      H[out] = d[0];
-      H[out + 1] = d[1];
+      poly_product<NB>(d, Q + mine, R + col);
+      *reinterpret_cast<double2*>(H + out) = make_double2(d[0], d[1]);
     }
-    cluster_sync();                                // Q everywhere
+    mbar_wait_bounded<true>(q_bar, (uint32_t)(it & 1), &s_abort);
+    __syncthreads();                               // Q whole, H
+    if (threadIdx.x == 0 && !last) mbar_arrive_expect_tx(q_bar, kOthers);
+    if (!last) {
+      poly_product<NB>(d, H + own, Q + col);
+      poly_spread<NB>(s_mat + ((it + 1) & 1) * kMat + at, d, q, r_bar);
+    }
     if (it > 0) {
-      poly_product<NB>(d, P[cur] + hi * C::kPitch + lo, Q + col + lo);
-      P[cur ^ 1][out] = d[0];
-      P[cur ^ 1][out + 1] = d[1];
+      poly_product<NB>(e, P[cur] + own, Q + col);
+      *reinterpret_cast<double2*>(P[cur ^ 1] + out) = make_double2(e[0], e[1]);
       cur ^= 1;
     }
     if (!last) {
-      poly_product<NB>(d, H + hi * C::kPitch + lo, Q + col + lo);
-      poly_spread<NB>(R + at, d);
-      cluster_sync();                              // R everywhere
+      mbar_wait_bounded<true>(r_bar, (uint32_t)(it & 1), &s_abort);
+      __syncthreads();                             // R of the next round whole
+      if (threadIdx.x == 0 && it + 2 < steps) mbar_arrive_expect_tx(r_bar, kOthers);
     }
   }
   __syncthreads();
   double* to = p.P + (mat * C::kRp + 8 * q) * (int64_t)C::kRp;
   for (int e = threadIdx.x; e < 8 * C::kRp; e += C::kThreads) to[e] = P[cur][e / C::kRp * C::kPitch + e % C::kRp];
+  cluster_sync();                                  // no CTA leaves while another may still send to it
 }
 
-// x = P u and the update.  A warp holds 32 long-side elements of u as 64-bit
-// fragments and goes through P's rows, kept in shared memory.  Which k-step an
-// index of the inner sum falls in, and which column of a block a long-side
-// (wide) or short-side (tall) index is, is chosen so that every lane reads and
-// writes runs of consecutive floats.
+// x = P u and the update.  A warp holds 16 long-side elements of u as 64-bit
+// fragments, and the master's values that it will update, before it waits for
+// the polynomial (the momentum was written two launches ago), then goes through
+// P's rows in shared memory.  Which k-step an index of the inner sum falls in,
+// and which column of a block a long-side (wide) or short-side (tall) index is,
+// is chosen so that every lane reads and writes runs of consecutive floats.
 constexpr int kApply64Threads = 128;
 template <int NB, bool kTall>
 __global__ void __launch_bounds__(kApply64Threads) muon_apply64_kernel(const MuonArgs p) {
@@ -339,124 +370,118 @@ __global__ void __launch_bounds__(kApply64Threads) muon_apply64_kernel(const Muo
   __shared__ __align__(16) double s_p[kRp * kPitch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
   const int64_t mat = blockIdx.y, base = mat * (int64_t)p.r * p.len;
-  const bool vec = kTall ? (p.r & 3) == 0 : (p.len & 3) == 0;
-  const int64_t blocks = (p.len + 31) / 32;
-  bool ready = false;
-  for (int64_t b0 = (int64_t)blockIdx.x * 4; b0 < blocks; b0 += (int64_t)gridDim.x * 4) {
-    const int64_t b = b0 + warp;
-    double f[4][KS];                               // [8 long-side elements][k-step]
-    if (b < blocks) {
-      // the momentum was written two launches ago: it may be read before the
-      // wait for the polynomial
-      if (!kTall) {
-        // k-step ks, lane: short index 4 ks + lo; block cb, lane: long index 4 hi + cb
-        const int64_t c = b * 32 + 4 * hi;
+  const bool vec = kTall ? (p.r & 3) == 0 : (p.len & 1) == 0;
+  const int64_t b = (int64_t)blockIdx.x * 4 + warp, c0 = b * 16;
+  double f[2][KS];                                 // [8 long-side elements][k-step]
+  float w[NB][4];                                  // [8 short-side (wide) or pair of 8 and 8 long-side (tall)][run]
+  int64_t at[NB];
+  int64_t have[NB];
+  if (!kTall) {
+    // k-step ks, lane: short index 4 ks + lo; block cb, lane: long index 2 hi + cb
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int row = 4 * k + lo;
-          const int64_t have = row < p.r ? p.len - c : 0, at = base + (int64_t)min(row, p.r - 1) * p.len + c;
-          float g[4], m[4];
-          load_run<4>(p.g + at, have, vec, g);
-          load_run<4>(p.m + at, have, vec, m);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e][k] = (double)muon_u(p, g[e], m[e]);
-        }
+    for (int k = 0; k < KS; ++k) {
+      const int row = 4 * k + lo;
+      const int64_t c = c0 + 2 * hi, n = row < p.r ? p.len - c : 0, x = base + (int64_t)min(row, p.r - 1) * p.len + c;
+      float2 g = make_float2(0.f, 0.f), m = g;
+      if (vec && n >= 2) {
+        g = __ldcg(reinterpret_cast<const float2*>(p.g + x));
+        m = __ldcg(reinterpret_cast<const float2*>(p.m + x));
       } else {
-        // k-step ks, lane: short index KS lo + ks; block cb, lane: long index 8 cb + hi
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t c = b * 32 + 8 * e + hi;
-          const int64_t have = c < p.len ? p.r - KS * lo : 0, at = base + min(c, p.len - 1) * p.r + KS * lo;
-          float g[KS], m[KS];
-          load_run<KS>(p.g + at, have, vec, g);
-          load_run<KS>(p.m + at, have, vec, m);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) f[e][k] = (double)muon_u(p, g[k], m[k]);
-        }
+        if (n > 0) { g.x = __ldcg(p.g + x); m.x = __ldcg(p.m + x); }
+        if (n > 1) { g.y = __ldcg(p.g + x + 1); m.y = __ldcg(p.m + x + 1); }
       }
+      f[0][k] = (double)muon_u(p, g.x, m.x);
+      f[1][k] = (double)muon_u(p, g.y, m.y);
     }
-    if (!ready) {
-      griddep_wait();
-      griddep_launch_dependents();
-      const double* P = p.P + mat * kRp * kRp;
-      for (int e = threadIdx.x; e < kRp * kRp; e += kApply64Threads) {
-        const int i = e / kRp, j = e % kRp;
-        if (!kTall) {
-          s_p[i * kPitch + j] = P[e];
-        } else {
-          // row: block ib, column n of short index i = 2 NB (n / 2) + 2 ib + n % 2; column: k-step order
-          const int n = i / (2 * NB) * 2 + (i & 1), ib = i % (2 * NB) / 2;
-          s_p[(8 * ib + n) * kPitch + 4 * (j % KS) + j / KS] = P[e];
-        }
-      }
-      __syncthreads();
-      ready = true;
+    // row block ib, lane: short index 8 ib + hi, long indices 4 lo + 0 .. 3
+#pragma unroll
+    for (int ib = 0; ib < NB; ++ib) {
+      const int row = 8 * ib + hi;
+      const int64_t c = c0 + 4 * lo;
+      have[ib] = row < p.r ? p.len - c : 0;
+      at[ib] = base + (int64_t)min(row, p.r - 1) * p.len + c;
+      load_run<4>(p.master + at[ib], have[ib], (p.len & 3) == 0, w[ib]);
     }
-    if (b >= blocks) continue;
-#pragma unroll 1
-    for (int ib = 0; ib < NB; ib += 2) {
-      float w[4][4] = {};                          // master values
-      int64_t at[4];
-      int64_t have[4];
+  } else {
+    // k-step ks, lane: short index KS lo + ks; block cb, lane: long index 8 cb + hi
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (!kTall) {
-          // rows ib and ib + 1, two runs of four each: e = 2 (row block) + run
-          const int row = 8 * (ib + e / 2) + hi;
-          const int64_t c = b * 32 + 8 * lo + 4 * (e & 1);
-          have[e] = row < p.r ? p.len - c : 0;
-          at[e] = base + (int64_t)min(row, p.r - 1) * p.len + c;
-        } else {
-          const int64_t c = b * 32 + 8 * e + hi;
-          const int i = 2 * NB * lo + 2 * ib;
-          have[e] = c < p.len ? p.r - i : 0;
-          at[e] = base + min(c, p.len - 1) * p.r + i;
-        }
-        load_run<4>(p.master + at[e], have[e], vec, w[e]);
-      }
-      double d[2][4][2] = {};                      // [row block][8 long-side elements][2]
-      const double* s0 = s_p + (8 * ib + hi) * kPitch + lo;
+    for (int e = 0; e < 2; ++e) {
+      const int64_t c = c0 + 8 * e + hi;
+      const int64_t n = c < p.len ? p.r - KS * lo : 0, x = base + min(c, p.len - 1) * p.r + KS * lo;
+      float g[KS], m[KS];
+      load_run<KS>(p.g + x, n, vec, g);
+      load_run<KS>(p.m + x, n, vec, m);
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const double x = s0[4 * k], y = s0[8 * kPitch + 4 * k];
+      for (int k = 0; k < KS; ++k) f[e][k] = (double)muon_u(p, g[k], m[k]);
+    }
+    // runs of four short indices 2 NB lo + 4 j .. of long index 8 e + hi; run e + 2 j
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!kTall) {
-            dmma(d[0][e], x, f[e][k]);
-            dmma(d[1][e], y, f[e][k]);
-          } else {
-            dmma(d[0][e], f[e][k], x);
-            dmma(d[1][e], f[e][k], y);
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // wide: long index 4 (2 lo + h) + cb, h = e & 1; tall: short index 2 NB lo + 2 (ib + i / 2) + i % 2
-          const float x = (float)(kTall ? d[i / 2][e][i & 1] : d[e / 2][i][e & 1]);
-          w[e][i] = __fmaf_rn(p.keep, w[e][i], -__fmul_rn(p.step, x));
-        }
-        store_run<4>(p.master + at[e], have[e], vec, w[e]);
-        if (vec && have[e] >= 4) {
-          const __nv_bfloat162 a = __floats2bfloat162_rn(w[e][0], w[e][1]), c = __floats2bfloat162_rn(w[e][2], w[e][3]);
-          *reinterpret_cast<uint2*>(p.w16 + at[e]) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < have[e]) {
-              const __nv_bfloat16 h = __float2bfloat16_rn(w[e][i]);
-              p.w16[at[e] + i] = *reinterpret_cast<const uint16_t*>(&h);
-            }
-        }
-      }
+    for (int i = 0; i < NB; ++i) {
+      const int64_t c = c0 + 8 * (i & 1) + hi;
+      const int s = 2 * NB * lo + 4 * (i >> 1);
+      have[i] = c < p.len ? p.r - s : 0;
+      at[i] = base + min(c, p.len - 1) * p.r + s;
+      load_run<4>(p.master + at[i], have[i], vec, w[i]);
     }
   }
-  if (!ready) {
-    griddep_wait();
-    griddep_launch_dependents();
+  griddep_wait();
+  griddep_launch_dependents();
+  const double* P = p.P + mat * kRp * kRp;
+#pragma unroll 8
+  for (int e = threadIdx.x; e < kRp * kRp; e += kApply64Threads) {
+    const int i = e / kRp, j = e % kRp;
+    if (!kTall) {
+      s_p[i * kPitch + j] = P[e];
+    } else {
+      // row: block ib, column n of short index i = 2 NB (n / 2) + 2 ib + n % 2; column: k-step order
+      const int n = i / (2 * NB) * 2 + (i & 1), ib = i % (2 * NB) / 2;
+      s_p[(8 * ib + n) * kPitch + 4 * (j % KS) + j / KS] = P[e];
+    }
+  }
+  __syncthreads();
+  if (c0 >= p.len) return;
+#pragma unroll
+  for (int ib = 0; ib < NB; ib += 2) {
+    double d[2][2][2] = {};                        // [row block][8 long-side elements][2]
+    const double* s0 = s_p + (8 * ib + hi) * kPitch + lo;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const double x = s0[4 * k], y = s0[8 * kPitch + 4 * k];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (!kTall) {
+          dmma(d[0][e], x, f[e][k]);
+          dmma(d[1][e], y, f[e][k]);
+        } else {
+          dmma(d[0][e], f[e][k], x);
+          dmma(d[1][e], f[e][k], y);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = ib + e;                        // run
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // wide: row block ib + e, long index 2 (2 lo + i / 2) + i % 2; tall: long block e, short index ... 2 (ib + i / 2) + i % 2
+        const float x = (float)(kTall ? d[i / 2][e][i & 1] : d[e][i & 1][i / 2]);
+        w[r][i] = __fmaf_rn(p.keep, w[r][i], -__fmul_rn(p.step, x));
+      }
+      const bool v4 = kTall ? vec : (p.len & 3) == 0;
+      store_run<4>(p.master + at[r], have[r], v4, w[r]);
+      if (v4 && have[r] >= 4) {
+        const __nv_bfloat162 lo2 = __floats2bfloat162_rn(w[r][0], w[r][1]), hi2 = __floats2bfloat162_rn(w[r][2], w[r][3]);
+        *reinterpret_cast<uint2*>(p.w16 + at[r]) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < have[r]) {
+            const __nv_bfloat16 h = __float2bfloat16_rn(w[r][i]);
+            p.w16[at[r] + i] = *reinterpret_cast<const uint16_t*>(&h);
+          }
+      }
+    }
   }
 }
 
