@@ -210,8 +210,8 @@ struct AdapterRows {
 __device__ __forceinline__ AdapterRows adapter_rows(const PoolArgs& p, int a, int width) {
   AdapterRows r{0, 0, 0.f};
   if (a < 0 || a >= p.n) return r;
-  const int f = p.first[a], k = p.rank[a];
-  const float scale = p.scale[a];                // (with the others, not behind them)
+  const int f = __ldcg(p.first + a), k = __ldcg(p.rank + a);
+  const float scale = __ldcg(p.scale + a);       // (with the others, not behind them)
   if (f < 0 || k < 1 || k > width || f > p.rows - ((k + 15) & ~15)) return r;
   r.first = f;
   r.rank = k;

@@ -65,7 +65,7 @@ struct RowLane {
 };
 __device__ __forceinline__ void row_tokens(RowLane& r, const int32_t* order, int first, int count, int i) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r.tok[j] = order[first + max(0, min(4 * i + j, count - 1))];
+  for (int j = 0; j < 4; ++j) r.tok[j] = __ldcg(order + first + max(0, min(4 * i + j, count - 1)));
 }
 __device__ __forceinline__ void row_whole(RowLane& r, int count, int i) {
   const int lane = threadIdx.x & 31;
@@ -128,6 +128,20 @@ struct Ring {
   }
 };
 
+// Four values of every CTA of the cluster, added in rank order, the loads together.
+template <int CS>
+__device__ __forceinline__ float4 cluster_sum(uint32_t at) {
+  float4 f[CS];
+#pragma unroll
+  for (int c = 0; c < CS; ++c) f[c] = ld_shared_cluster_f4(mapa_shared(at, (uint32_t)c));
+  float4 v = f[0];
+#pragma unroll
+  for (int c = 1; c < CS; ++c) {
+    v.x += f[c].x; v.y += f[c].y; v.z += f[c].z; v.w += f[c].w;
+  }
+  return v;
+}
+
 // ---------------------------------------------------------------------- shrink
 struct ShrinkArgs {
   const int32_t* order;
@@ -156,22 +170,11 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = (int)(blockIdx.x % p.csize), u = (int)(blockIdx.x / p.csize);
-  griddep_wait();
-  griddep_launch_dependents();
-  const int4 tile = p.tiles[u];
-  if (tile.z <= 0) return;                       // the whole cluster
-  const int count = min(tile.z, kReqTile);
-  const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
-  if (ad.rank == 0) {
-    if (p.U && q == 0)
-      for (int e = threadIdx.x; e < count * p.width; e += kShrinkThreads)
-        p.U[(int64_t)p.order[tile.y + e / p.width] * p.width + e % p.width] = 0.f;
-    return;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&box);
+    tma_prefetch_desc(&row);
+    tma_prefetch_desc(&weight);
   }
-  const int r16 = (ad.rank + 15) & ~15;
-  const int kper = ((p.K + p.csize - 1) / p.csize + 63) / 64 * 64;
-  const int k0 = min(p.K, q * kper), k1 = min(p.K, k0 + kper);
-  const int steps = (k1 - k0 + 63) / 64;
   volatile int* abort_flag = &s_abort;
 
   Ring ring;
@@ -199,6 +202,27 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  griddep_wait();
+  // (behind the allocation: a dependent that allocates early must not take Tensor Memory this CTA still needs)
+  griddep_launch_dependents();
+  const int4 tile = p.tiles[u];
+  if (tile.z <= 0) {                             // the whole cluster
+    if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+    return;
+  }
+  const int count = min(tile.z, kReqTile);
+  const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
+  if (ad.rank == 0) {
+    if (p.U && q == 0)
+      for (int e = threadIdx.x; e < count * p.width; e += kShrinkThreads)
+        p.U[(int64_t)p.order[tile.y + e / p.width] * p.width + e % p.width] = 0.f;
+    if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+    return;
+  }
+  const int r16 = (ad.rank + 15) & ~15;
+  const int kper = ((p.K + p.csize - 1) / p.csize + 63) / 64 * 64;
+  const int k0 = min(p.K, q * kper), k1 = min(p.K, k0 + kper);
+  const int steps = (k1 - k0 + 63) / 64;
 
   if (warp == 0) {
     const RowLane r = row_lane(p.order, tile.y, count, lane);
@@ -303,14 +327,14 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
     const int i = q * rows + e / w4, j = (e % w4) * 4;
     const bool valid = i < count;
     const int64_t tok = valid ? p.order[tile.y + i] : 0;
+    float4 saved = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.V_in && valid && j < r16) saved = *reinterpret_cast<const float4*>(p.U_in + tok * p.width + j);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (valid && j < r16) {
       const uint32_t at = part + (uint32_t)(i * pitch + j) * 4u;
-      for (int c = 0; c < p.csize; ++c) {
-        const float4 f = p.csize > 1 ? ld_shared_cluster_f4(mapa_shared(at, (uint32_t)c))
-                                     : *reinterpret_cast<const float4*>(s_part + i * pitch + j);
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-      }
+      const float4 f = p.csize == 8 ? cluster_sum<8>(at) : p.csize == 4 ? cluster_sum<4>(at) : p.csize == 2 ? cluster_sum<2>(at)
+                       : *reinterpret_cast<const float4*>(s_part + i * pitch + j);
+      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 #pragma unroll
       for (int n = 0; n < 4; ++n)
         if (j + n >= ad.rank) v[n] = 0.f;
@@ -322,11 +346,7 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
       for (int n = 0; n < 4; ++n) v[n] = __fmul_rn(ad.scale, v[n]);
       store_terms(p.V + vrow, j, r16, v);
       if (p.V_in) {
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        if (valid) {
-          const float4 f = *reinterpret_cast<const float4*>(p.U_in + tok * p.width + j);
-          w[0] = f.x; w[1] = f.y; w[2] = f.z; w[3] = f.w;
-        }
+        float w[4] = {saved.x, saved.y, saved.z, saved.w};
 #pragma unroll
         for (int n = 0; n < 4; ++n) w[n] = j + n < ad.rank ? __fmul_rn(ad.scale, w[n]) : 0.f;
         store_terms(p.V_in + vrow, j, r16, w);
@@ -362,23 +382,29 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = (int)(blockIdx.x / p.ranges);
   const int n0 = (int)(blockIdx.x % p.ranges) * p.range, n1 = min(p.N, n0 + p.range);
-  griddep_wait();
-  griddep_launch_dependents();
-  const int4 tile = p.tiles[u];
-  if (tile.z <= 0) return;
+  // Everything but V was there before the kernel in front started, which waited
+  // for it: only V waits here.  (Maps and tables past L1.)
+  const int4 tile = __ldcg(p.tiles + u);
+  if (tile.z <= 0) {
+    griddep_wait();
+    return;
+  }
   const int count = min(tile.z, kReqTile);
   const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
   if (ad.rank == 0) {
     if (p.out != p.base) {
       // the base's rows as they are, eight 16-byte words of a thread in flight
       const int n8 = (n1 - n0) / 8;
+      int* s_tok = reinterpret_cast<int*>(smem);
+      for (int i = threadIdx.x; i < count; i += kReqThreads) s_tok[i] = __ldcg(p.order + tile.y + i);
+      __syncthreads();
       for (int e0 = threadIdx.x; e0 < count * n8; e0 += 8 * kReqThreads) {
         uint4 v[8];
         int64_t at[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int e = min(e0 + i * kReqThreads, count * n8 - 1);
-          at[i] = (int64_t)p.order[tile.y + e / n8] * p.N + n0 + (e % n8) * 8;
+          at[i] = (int64_t)s_tok[e / n8] * p.N + n0 + (e % n8) * 8;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = p.base ? *reinterpret_cast<const uint4*>(p.base + at[i]) : make_uint4(0, 0, 0, 0);
@@ -387,6 +413,7 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
           if (e0 + i * kReqThreads < count * n8) *reinterpret_cast<uint4*>(p.out + at[i]) = v[i];
       }
     }
+    griddep_wait();
     return;
   }
   const int r16 = (ad.rank + 15) & ~15;
@@ -420,20 +447,28 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();                   // (behind the allocation, as above)
   const uint32_t tmem = s_tmem;
 
   if (warp == 0) {
     const RowLane r = row_lane(p.order, tile.y, count, lane);
     const uint32_t bytes = (p.base ? row_bytes(count) : 0u) + (uint32_t)r16 * 128u;
-    // V: hi and mid of every 64 of the rank, in boxes of 64 columns
-    if (lane == 0) {
-      const int boxes = 2 * ((r16 + 63) / 64);
-      mbar_arrive_expect_tx(v_bar, (uint32_t)(boxes * kReqRows));
-      for (int i = 0; i < boxes; ++i)
-        tma_load_2d(sbase + (uint32_t)(i * kReqRows), &terms, v_bar, (i >> 1) * 192 + (i & 1) * 64, u * kReqTile);
-    }
     int issued = 0;
+    bool v_issued = false;
+    // V: hi and mid of every 64 of the rank, in boxes of 64 columns; behind the first stages' loads
+    auto load_v = [&] {
+      griddep_wait();
+      v_issued = true;
+      if (lane == 0) {
+        const int boxes = 2 * ((r16 + 63) / 64);
+        mbar_arrive_expect_tx(v_bar, (uint32_t)(boxes * kReqRows));
+        for (int i = 0; i < boxes; ++i)
+          tma_load_2d(sbase + (uint32_t)(i * kReqRows), &terms, v_bar, (i >> 1) * 192 + (i & 1) * 64, u * kReqTile);
+      }
+      __syncwarp();
+    };
     for (int s = 0; s < chunks; ++s) {
+      if (s == min(p.stages, chunks - 1)) load_v();
       int ok = 1;
       if (lane == 0) {
         ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
@@ -448,8 +483,9 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
       ring.next();
       ++issued;
     }
+    if (!v_issued) griddep_wait();
     if (*abort_flag && lane == 0) {
-      mbar_wait_bounded(v_bar, 0, nullptr);
+      if (v_issued) mbar_wait_bounded(v_bar, 0, nullptr);
       for (int i = 0; i < min(issued, p.stages); ++i) {
         const int last = (issued - 1 - i) / p.stages;
         mbar_wait_bounded(ring.full + 8u * i, (uint32_t)(last & 1), nullptr);
@@ -489,7 +525,7 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
     if (!ok && any) mbar_wait_bounded(acc_full + 8u * last, 0, nullptr);
   } else if (warp >= 2) {
     const int quarter = warp & 3, rowi = quarter * 32 + lane;
-    const int tok = p.order[tile.y + min(rowi, count - 1)];
+    const int tok = __ldcg(p.order + tile.y + min(rowi, count - 1));
     for (int s = 0; s < chunks; ++s) {
       const int buf = s & 1;
       bool ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag) &&
@@ -694,14 +730,6 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
     *abort_flag = 0;
     fence_mbar_init();
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  grad_locate(p, s_scan, (int)blockIdx.x, (int)gridDim.x);
-  const long long at = s_scan.at, total = s_scan.total;
-  const int parts = s_scan.parts;
-  const long long left0 = (int)blockIdx.x < parts ? total * (blockIdx.x + 1) / parts - at : 0;
-  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (left0 <= 0) return;
   if (warp == 1) {
     tmem_alloc(smem_u32(&s_tmem), (uint32_t)p.tmem_cols);
     tmem_relinquish();
@@ -709,7 +737,18 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();
   const uint32_t tmem = s_tmem;
+  griddep_wait();
+  grad_locate(p, s_scan, (int)blockIdx.x, (int)gridDim.x);
+  const long long at = s_scan.at, total = s_scan.total;
+  const int parts = s_scan.parts;
+  const long long left0 = (int)blockIdx.x < parts ? total * (blockIdx.x + 1) / parts - at : 0;
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (left0 <= 0) {
+    if (warp == 1) tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+    return;
+  }
   GradUnit g;
   grad_adapter(p, g, s_scan.a);
   g.unit = (int)((at - s_scan.base) / g.steps);
