@@ -33,7 +33,8 @@
 namespace qlora {
 
 constexpr int kReqTile = 128;
-constexpr int kReqThreads = 192;             // warp 0: TMA, warp 1: MMA, warps 2-5: epilogue
+// warp 0: TMA, warp 1: MMA, the others: epilogue
+constexpr int kExpandThreads = 320;          // warps 2-9: epilogue, 32 rows x 32 columns of a stage each
 constexpr int kShrinkThreads = 320;          // warps 2-9: epilogue, two per quarter of the rows
 constexpr int kReqRows = 128 * 128;          // bytes of 128 rows x 64 bf16 columns
 
@@ -360,85 +361,84 @@ __global__ void __launch_bounds__(kShrinkThreads) requests_shrink_kernel(const _
 struct ExpandArgs {
   const int32_t* order;
   const int4* tiles;
+  const int32_t* n_tiles;
   PoolArgs pool;
-  int N, width, range, ranges, stages, stage_bytes, v_bytes;
+  int N, width, stages, stage_bytes, v_bytes;
   const uint16_t* base;
   uint16_t* out;
 };
 
+// A CTA's share: pieces of consecutive 64-column blocks of one tile each.  The
+// blocks of all tiles, tile by tile, are cut into equal parts, one per CTA, so
+// no CTA starts late or ends early and set-up and first loads are paid once.
+struct ExpandPiece {
+  long long at, end;            // blocks left to this CTA
+  int chunks;                   // blocks of a tile
+  int u, c, count_c;            // the piece: tile, first block, blocks
+  int4 tile;
+  AdapterRows ad;
+};
+__device__ __forceinline__ bool expand_piece(const ExpandArgs& p, ExpandPiece& s) {
+  if (s.at >= s.end) return false;
+  s.u = (int)(s.at / s.chunks);
+  s.c = (int)(s.at % s.chunks);
+  s.count_c = (int)min((long long)(s.chunks - s.c), s.end - s.at);
+  s.at += s.count_c;
+  // (maps and tables past L1: they are read ahead of the dependency wait)
+  s.tile = __ldcg(p.tiles + s.u);
+  s.tile.z = min(s.tile.z, kReqTile);
+  s.ad = adapter_rows(p.pool, s.tile.x, p.width);
+  return true;
+}
+__device__ __forceinline__ ExpandPiece expand_share(const ExpandArgs& p) {
+  ExpandPiece s;
+  s.chunks = (p.N + 63) / 64;
+  const long long all = (long long)__ldcg(p.n_tiles) * s.chunks;
+  s.at = all * blockIdx.x / gridDim.x;
+  s.end = all * (blockIdx.x + 1) / gridDim.x;
+  return s;
+}
+
 // Streams base in and Y out, 64 columns of the tile's rows a stage, with a few
 // small MMAs (two per 16 of the rank) in between: HBM-bound.
-__global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __grid_constant__ CUtensorMap box,
-                                                                      const __grid_constant__ CUtensorMap row,
-                                                                      const __grid_constant__ CUtensorMap weight,
-                                                                      const __grid_constant__ CUtensorMap terms,
-                                                                      const __grid_constant__ ExpandArgs p) {
+__global__ void __launch_bounds__(kExpandThreads, 2) requests_expand_kernel(const __grid_constant__ CUtensorMap box,
+                                                                            const __grid_constant__ CUtensorMap row,
+                                                                            const __grid_constant__ CUtensorMap weight,
+                                                                            const __grid_constant__ CUtensorMap terms,
+                                                                            const __grid_constant__ ExpandArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 5];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 6];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = (int)(blockIdx.x / p.ranges);
-  const int n0 = (int)(blockIdx.x % p.ranges) * p.range, n1 = min(p.N, n0 + p.range);
-  // Everything but V was there before the kernel in front started, which waited
-  // for it: only V waits here.  (Maps and tables past L1.)
-  const int4 tile = __ldcg(p.tiles + u);
-  if (tile.z <= 0) {
-    griddep_wait();
-    return;
-  }
-  const int count = min(tile.z, kReqTile);
-  const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
-  if (ad.rank == 0) {
-    if (p.out != p.base) {
-      // the base's rows as they are, eight 16-byte words of a thread in flight
-      const int n8 = (n1 - n0) / 8;
-      int* s_tok = reinterpret_cast<int*>(smem);
-      for (int i = threadIdx.x; i < count; i += kReqThreads) s_tok[i] = __ldcg(p.order + tile.y + i);
-      __syncthreads();
-      for (int e0 = threadIdx.x; e0 < count * n8; e0 += 8 * kReqThreads) {
-        uint4 v[8];
-        int64_t at[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = min(e0 + i * kReqThreads, count * n8 - 1);
-          at[i] = (int64_t)s_tok[e / n8] * p.N + n0 + (e % n8) * 8;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = p.base ? *reinterpret_cast<const uint4*>(p.base + at[i]) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e0 + i * kReqThreads < count * n8) *reinterpret_cast<uint4*>(p.out + at[i]) = v[i];
-      }
-    }
-    griddep_wait();
-    return;
-  }
-  const int r16 = (ad.rank + 15) & ~15;
-  const int chunks = (n1 - n0 + 63) / 64;
   volatile int* abort_flag = &s_abort;
 
   Ring ring;
   ring.full = smem_u32(&s_bar[0]);
   ring.empty = smem_u32(&s_bar[8]);
   ring.stages = p.stages;
-  const uint32_t v_bar = smem_u32(&s_bar[16]);
-  const uint32_t acc_full = smem_u32(&s_bar[17]), acc_empty = smem_u32(&s_bar[19]);   // two each
+  const uint32_t v_full = smem_u32(&s_bar[16]), v_empty = smem_u32(&s_bar[17]);
+  const uint32_t acc_full = smem_u32(&s_bar[18]), acc_empty = smem_u32(&s_bar[20]);   // two each
   const uint32_t stage0 = sbase + (uint32_t)p.v_bytes;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(ring.full + 8u * i, 1);
-      mbar_init(ring.empty + 8u * i, 4);
+      mbar_init(ring.empty + 8u * i, 8);
     }
-    mbar_init(v_bar, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8u * i, 1);
-      mbar_init(acc_empty + 8u * i, 4);
+      mbar_init(acc_empty + 8u * i, 8);
     }
     *abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&box);
+    tma_prefetch_desc(&row);
+    tma_prefetch_desc(&weight);
+    tma_prefetch_desc(&terms);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&s_tmem), 128);
@@ -449,134 +449,177 @@ __global__ void __launch_bounds__(kReqThreads) requests_expand_kernel(const __gr
   tc_fence_after();
   griddep_launch_dependents();                   // (behind the allocation, as above)
   const uint32_t tmem = s_tmem;
+  // Everything but V was there before the kernel in front started, which waited
+  // for it: only V's loads wait for that kernel.
+  ExpandPiece s = expand_share(p);
 
   if (warp == 0) {
-    const RowLane r = row_lane(p.order, tile.y, count, lane);
-    const uint32_t bytes = (p.base ? row_bytes(count) : 0u) + (uint32_t)r16 * 128u;
-    int issued = 0;
-    bool v_issued = false;
-    // V: hi and mid of every 64 of the rank, in boxes of 64 columns; behind the first stages' loads
-    auto load_v = [&] {
-      griddep_wait();
-      v_issued = true;
-      if (lane == 0) {
-        const int boxes = 2 * ((r16 + 63) / 64);
-        mbar_arrive_expect_tx(v_bar, (uint32_t)(boxes * kReqRows));
-        for (int i = 0; i < boxes; ++i)
-          tma_load_2d(sbase + (uint32_t)(i * kReqRows), &terms, v_bar, (i >> 1) * 192 + (i & 1) * 64, u * kReqTile);
+    int issued = 0, pieces = 0, ok = 1;
+    bool waited = false;
+    while (ok && expand_piece(p, s)) {
+      if (s.ad.rank == 0) continue;
+      const int count = s.tile.z, r16 = (s.ad.rank + 15) & ~15;
+      const RowLane r = row_lane(p.order, s.tile.y, count, lane);
+      const uint32_t bytes = (p.base ? row_bytes(count) : 0u) + (uint32_t)r16 * 128u;
+      // V: hi and mid of every 64 of the rank; for the first piece behind the first stages' loads
+      auto load_v = [&] {
+        if (!waited) griddep_wait();
+        waited = true;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(v_empty, (uint32_t)((pieces & 1) ^ 1), abort_flag);
+          if (ok) {
+            const int boxes = 2 * ((r16 + 63) / 64);
+            mbar_arrive_expect_tx(v_full, (uint32_t)(boxes * kReqRows));
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(sbase + (uint32_t)(i * kReqRows), &terms, v_full, (i >> 1) * 192 + (i & 1) * 64, s.u * kReqTile);
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      };
+      const int v_at = min(waited ? 1 : p.stages, s.count_c - 1);
+      for (int c = 0; c < s.count_c; ++c) {
+        if (c == v_at) load_v();
+        if (!ok) break;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
+          if (ok) mbar_arrive_expect_tx(ring.full_bar(), bytes);
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        const uint32_t st = stage0 + (uint32_t)(ring.at * p.stage_bytes);
+        const int x = (s.c + c) * 64;
+        if (p.base) load_rows(st, &box, &row, ring.full_bar(), x, r, lane, count);
+        if (lane < r16 / 16)
+          tma_load_2d(st + kReqRows + (uint32_t)lane * 2048u, &weight, ring.full_bar(), x, s.ad.first + 16 * lane);
+        ring.next();
+        ++issued;
       }
-      __syncwarp();
-    };
-    for (int s = 0; s < chunks; ++s) {
-      if (s == min(p.stages, chunks - 1)) load_v();
-      int ok = 1;
-      if (lane == 0) {
-        ok = mbar_wait_bounded(ring.empty_bar(), ring.phase ^ 1u, abort_flag);
-        if (ok) mbar_arrive_expect_tx(ring.full_bar(), bytes);
-      }
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-      const uint32_t st = stage0 + (uint32_t)(ring.at * p.stage_bytes);
-      const int x = n0 + s * 64;
-      if (p.base) load_rows(st, &box, &row, ring.full_bar(), x, r, lane, count);
-      if (lane < r16 / 16)
-        tma_load_2d(st + kReqRows + (uint32_t)lane * 2048u, &weight, ring.full_bar(), x, ad.first + 16 * lane);
-      ring.next();
-      ++issued;
+      ++pieces;
     }
-    if (!v_issued) griddep_wait();
+    if (!waited) griddep_wait();
     if (*abort_flag && lane == 0) {
-      if (v_issued) mbar_wait_bounded(v_bar, 0, nullptr);
+      // copies in flight: the last piece's V may or may not have been asked for
       for (int i = 0; i < min(issued, p.stages); ++i) {
         const int last = (issued - 1 - i) / p.stages;
         mbar_wait_bounded(ring.full + 8u * i, (uint32_t)(last & 1), nullptr);
       }
+      if (pieces > 0) mbar_wait_bounded(v_full, (uint32_t)((pieces - 1) & 1), nullptr);
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_bf16_f32(128, 64, 0, 1);
     const uint64_t v0 = smem_desc_sw128(sbase, 16, 1024), w0 = smem_desc_sw128(stage0 + kReqRows, 8192, 1024);
-    bool ok = mbar_wait_bounded(v_bar, 0, abort_flag);
-    int any = 0, last = 0;
-    for (int s = 0; s < chunks && ok; ++s) {
-      const int buf = s & 1;
-      ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((s >> 1) & 1) ^ 1), abort_flag) &&
-           mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(buf * 64);
-      const uint64_t w = w0 + ((uint32_t)(ring.at * p.stage_bytes) >> 4);
-      uint32_t acc = 0;
-      for (int c = 0; c < r16; c += 64) {
-        const int ks = min(64, r16 - c) / 16;
-        // hi, then mid (a box further); 16 of the rank are 32 bytes of V's rows and 16 rows of the factor
-        const uint64_t v = v0 + (uint64_t)(c / 64 * (2 * kReqRows / 16)), wc = w + (uint64_t)(c * 8);
+    bool ok = true;
+    int n = 0, pieces = 0;
+    while (ok && expand_piece(p, s)) {
+      if (s.ad.rank == 0) continue;
+      const int r16 = (s.ad.rank + 15) & ~15;
+      ok = mbar_wait_bounded(v_full, (uint32_t)(pieces & 1), abort_flag);
+      ++pieces;
+      for (int c = 0; c < s.count_c && ok; ++c, ++n) {
+        const int buf = n & 1;
+        ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag) &&
+             mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * 64);
+        const uint64_t w = w0 + ((uint32_t)(ring.at * p.stage_bytes) >> 4);
+        uint32_t acc = 0;
+        for (int j = 0; j < r16; j += 64) {
+          const int ks = min(64, r16 - j) / 16;
+          // hi, then mid (a box further); 16 of the rank are 32 bytes of V's rows and 16 rows of the factor
+          const uint64_t v = v0 + (uint64_t)(j / 64 * (2 * kReqRows / 16)), wj = w + (uint64_t)(j * 8);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < ks) {
-            umma_bf16(d, v + (uint64_t)(2 * k), wc + (uint64_t)(128 * k), idesc, acc);
-            acc = 1;
-            umma_bf16(d, v + (uint64_t)(kReqRows / 16 + 2 * k), wc + (uint64_t)(128 * k), idesc, 1u);
-          }
-      }
-      any = 1;
-      last = buf;
-      umma_commit(acc_full + 8u * buf);
-      ring.next();
-    }
-    if (!ok && any) mbar_wait_bounded(acc_full + 8u * last, 0, nullptr);
-  } else if (warp >= 2) {
-    const int quarter = warp & 3, rowi = quarter * 32 + lane;
-    const int tok = __ldcg(p.order + tile.y + min(rowi, count - 1));
-    for (int s = 0; s < chunks; ++s) {
-      const int buf = s & 1;
-      bool ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((s >> 1) & 1), abort_flag) &&
-                mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      tc_fence_after();
-      uint32_t v[64];
-      {
-        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
-        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
-        const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 64);
-        tmem_ld_32x32b_x32(t, lo);
-        tmem_ld_32x32b_x32(t + 32, hi);
-        tmem_ld_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
-      // base + term, in place in the stage (128B-swizzled rows: conflict-free)
-      uint8_t* st = smem + p.v_bytes + ring.at * p.stage_bytes;
-      uint8_t* mine = st + rowi * 128;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint4* at = reinterpret_cast<uint4*>(mine + ((c ^ (rowi & 7)) << 4));
-        uint4 b = p.base ? *at : make_uint4(0, 0, 0, 0);
-        uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(w[j]) + __uint_as_float(v[8 * c + 2 * j]),
-                                                         bf_hi(w[j]) + __uint_as_float(v[8 * c + 2 * j + 1]));
-          w[j] = *reinterpret_cast<const uint32_t*>(&o);
+          for (int k = 0; k < 4; ++k)
+            if (k < ks) {
+              umma_bf16(d, v + (uint64_t)(2 * k), wj + (uint64_t)(128 * k), idesc, acc);
+              acc = 1;
+              umma_bf16(d, v + (uint64_t)(kReqRows / 16 + 2 * k), wj + (uint64_t)(128 * k), idesc, 1u);
+            }
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c == s.count_c - 1) umma_commit(v_empty);
+        umma_commit(acc_full + 8u * buf);
+        ring.next();
       }
-      __syncwarp();
-      const int x = n0 + s * 64 + (lane & 7) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = quarter * 32 + i * 4 + lane / 8;
-        const int64_t t = __shfl_sync(0xFFFFFFFFu, tok, i * 4 + lane / 8);
-        if (r < count && x < n1)
-          *reinterpret_cast<uint4*>(p.out + t * p.N + x) =
-              *reinterpret_cast<const uint4*>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-      }
-      fence_proxy_async_smem();                  // the next copy into this stage comes by TMA
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ring.empty_bar());
-      ring.next();
     }
+    if (!ok && n > 0) mbar_wait_bounded(acc_full + 8u * ((n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), nullptr);
+  } else if (warp >= 2) {
+    const int quarter = warp & 3, half = (warp - 2) >> 2, rowi = quarter * 32 + lane;
+    bool ok = true;
+    int n = 0;
+    while (ok && expand_piece(p, s)) {
+      const int count = s.tile.z, x0 = s.c * 64, x1 = min(p.N, x0 + s.count_c * 64);
+      if (s.ad.rank == 0) {
+        // no adapter: the base's rows as they are, eight 16-byte words of a lane in flight
+        if (p.out == p.base) continue;
+        // (the warp's rows are warp - 2 + 8 j, row j's token in lane j)
+        const int rows = (count - (warp - 2) + 7) / 8, words = (x1 - x0) / 8, total = max(0, rows) * words;
+        const int tok = lane < rows ? __ldcg(p.order + s.tile.y + warp - 2 + 8 * lane) : 0;
+        for (int e0 = 0; e0 < total; e0 += 8 * 32) {
+          uint4 v[8];
+          int64_t at[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = min(e0 + 32 * i + lane, total - 1);
+            at[i] = (int64_t)__shfl_sync(0xFFFFFFFFu, tok, e / words) * p.N + x0 + (e % words) * 8;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = p.base ? __ldcs(reinterpret_cast<const uint4*>(p.base + at[i])) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e0 + 32 * i + lane < total) __stcs(reinterpret_cast<uint4*>(p.out + at[i]), v[i]);
+        }
+        continue;
+      }
+      const int tok = __ldcg(p.order + s.tile.y + min(rowi, count - 1));
+      for (int c = 0; c < s.count_c; ++c, ++n) {
+        const int buf = n & 1;
+        ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((n >> 1) & 1), abort_flag) &&
+             mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 64 + half * 32), v);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
+        // base + term, in place in the stage (128B-swizzled rows: conflict-free)
+        uint8_t* st = smem + p.v_bytes + ring.at * p.stage_bytes;
+        uint8_t* mine = st + rowi * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(mine + (((4 * half + i) ^ (rowi & 7)) << 4));
+          uint4 b = p.base ? *at : make_uint4(0, 0, 0, 0);
+          uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(w[j]) + __uint_as_float(v[8 * i + 2 * j]),
+                                                           bf_hi(w[j]) + __uint_as_float(v[8 * i + 2 * j + 1]));
+            w[j] = *reinterpret_cast<const uint32_t*>(&o);
+          }
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        // this warp's 32 rows x 64 bytes, eight rows at a time
+        const int piece = 4 * half + (lane & 3), x = x0 + c * 64 + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = quarter * 32 + i * 8 + lane / 4;
+          const int64_t t = __shfl_sync(0xFFFFFFFFu, tok, i * 8 + lane / 4);
+          if (r < count && x < x1)
+            __stcs(reinterpret_cast<uint4*>(p.out + t * p.N + x),
+                   *reinterpret_cast<const uint4*>(st + r * 128 + ((piece ^ (r & 7)) << 4)));
+        }
+        fence_proxy_async_smem();                // the next copy into this stage comes by TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ring.empty_bar());
+        ring.next();
+      }
+    }
+    tc_fence_before();
   }
-  tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 128);
 }
