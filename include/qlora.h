@@ -364,6 +364,24 @@ QLORA_API int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* 
                                 const float* U_saved, const uint16_t* dY, const uint16_t* base, uint16_t* dX, float* dA,
                                 float* dBt, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
 
+/*
+ * The whole layer on an NF4 base: lora_requests_fwd / _bwd with the base
+ * product (Y = X W'^T, dX = dY W') formed by the dequantising GEMMs first, in
+ * Y and dX themselves.  Rows without an adapter, those behind the last
+ * request among them, hold the base product (rounded to bf16 once; the others
+ * a second time with their adapter's term).  pool's k and d are q's.
+ */
+QLORA_API size_t qlora_fwd_requests_workspace_bytes(const qlora_nf4_t* q, const lora_pool_t* pool,
+                                                    const lora_requests_t* req);
+QLORA_API int qlora_fwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req,
+                                 const uint16_t* X, uint16_t* Y, float* U_save, void* workspace,
+                                 size_t workspace_bytes, qlora_stream_t stream);
+QLORA_API size_t qlora_bwd_requests_workspace_bytes(const qlora_nf4_t* q, const lora_pool_t* pool,
+                                                    const lora_requests_t* req);
+QLORA_API int qlora_bwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req,
+                                 const uint16_t* X, const float* U_saved, const uint16_t* dY, uint16_t* dX, float* dA,
+                                 float* dBt, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
 /* ------------------------------------------- plain LoRA on a bf16 base */
 
 /*

@@ -102,6 +102,10 @@ _SIGNATURES = {
     "lora_requests_fwd": (_INT, [_POOLP, _REQP, _VP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
     "lora_requests_bwd_workspace_bytes": (_SIZE, [_POOLP, _REQP]),
     "lora_requests_bwd": (_INT, [_POOLP, _REQP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
+    "qlora_fwd_requests_workspace_bytes": (_SIZE, [_NF4P, _POOLP, _REQP]),
+    "qlora_fwd_requests": (_INT, [_NF4P, _POOLP, _REQP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
+    "qlora_bwd_requests_workspace_bytes": (_SIZE, [_NF4P, _POOLP, _REQP]),
+    "qlora_bwd_requests": (_INT, [_NF4P, _POOLP, _REQP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SIZE, _VP]),
     "lora_muon_workspace_bytes": (_SIZE, [_I64, _I64, _I64]),
     "lora_muon_step": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _F, _F, _INT, _F, _F, _F, _INT, _VP, _VP, _SIZE,
                               _VP]),
@@ -588,7 +592,17 @@ def _cuda_device(device) -> torch.device:
     return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
 
 
-class AdapterPool:
+class _Held:
+    """Its tensors' addresses are in a C struct: they are written into, never
+    replaced."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be replaced; write into the tensor")
+        object.__setattr__(self, name, value)
+
+
+class AdapterPool(_Held):
     """The adapters of one linear as rows of two matrices (the lora_pool_t):
     A (rows x k) and Bt (rows x d, B transposed), bf16.  Adapter a of rank r
     has rows first[a] .. first[a] + r; the rows up to the next multiple of 16
@@ -642,7 +656,7 @@ class AdapterPool:
         self.Bt[rows].copy_(B.t())
 
 
-class RequestPlan:
+class RequestPlan(_Held):
     """Device buffers of a batch's maps (the lora_requests_t): n_req requests
     over T rows and pools of n adapters; see lora_requests_plan."""
 
@@ -743,6 +757,65 @@ def lora_requests_bwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, U_s
     return dX, dA, dBt
 
 
+def _need_base(q: NF4Weight, pool: AdapterPool):
+    if (q.d, q.k) != (pool.d, pool.k):
+        raise ValueError(f"weight {q.d} x {q.k}, pool for {pool.d} x {pool.k}")
+    if q.codes.device != pool.device:
+        raise ValueError(f"weight on {q.codes.device}, pool on {pool.device}")
+
+
+def qlora_fwd_requests_workspace_bytes(q: NF4Weight, pool: AdapterPool, plan: RequestPlan) -> int:
+    return lib().qlora_fwd_requests_workspace_bytes(ctypes.byref(q.cstruct), pool._ref, plan._ref)
+
+
+def qlora_bwd_requests_workspace_bytes(q: NF4Weight, pool: AdapterPool, plan: RequestPlan) -> int:
+    return lib().qlora_bwd_requests_workspace_bytes(ctypes.byref(q.cstruct), pool._ref, plan._ref)
+
+
+def qlora_fwd_requests(q: NF4Weight, pool: AdapterPool, plan: RequestPlan, X: torch.Tensor,
+                       Y: Optional[torch.Tensor] = None, U_save: Optional[torch.Tensor] = None, save: bool = False,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The layer on the NF4 weight with each request's adapter: Y, and U for
+    the backward with ``save`` (or U_save given)."""
+    _need_match(pool, plan)
+    _need_base(q, pool)
+    dev, T, bf = pool.device, plan.T, torch.bfloat16
+    xp = _need_on(X, bf, (T, pool.k), dev, "X")
+    with _On(dev, stream) as st:
+        Y = torch.empty(T, pool.d, dtype=bf, device=dev) if Y is None else Y
+        if U_save is None and save:
+            U_save = torch.zeros(T, pool.width, dtype=torch.float32, device=dev)
+        yp = _need_on(Y, bf, (T, pool.d), dev, "Y")
+        up = None if U_save is None else _need_on(U_save, torch.float32, (T, pool.width), dev, "U_save")
+        ws = workspace(qlora_fwd_requests_workspace_bytes(q, pool, plan), dev) if ws is None else _need_ws(ws, dev)
+        _check(lib().qlora_fwd_requests(ctypes.byref(q.cstruct), pool._ref, plan._ref, xp, yp, up, ws.data_ptr(),
+                                        ws.numel(), st), "qlora_fwd_requests")
+    return Y, U_save
+
+
+def qlora_bwd_requests(q: NF4Weight, pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, U_saved: torch.Tensor,
+                       dY: torch.Tensor, dX: Optional[torch.Tensor] = None, dA: Optional[torch.Tensor] = None,
+                       dBt: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Backward of qlora_fwd_requests: dX, and dA (rows x k), dBt (rows x d) of the pool's rows."""
+    _need_match(pool, plan)
+    _need_base(q, pool)
+    dev, T, bf, f32 = pool.device, plan.T, torch.bfloat16, torch.float32
+    xp = _need_on(X, bf, (T, pool.k), dev, "X")
+    up = _need_on(U_saved, f32, (T, pool.width), dev, "U_saved")
+    gp = _need_on(dY, bf, (T, pool.d), dev, "dY")
+    with _On(dev, stream) as st:
+        dX = torch.empty(T, pool.k, dtype=bf, device=dev) if dX is None else dX
+        dA = torch.empty(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
+        dBt = torch.empty(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
+        dxp = _need_on(dX, bf, (T, pool.k), dev, "dX")
+        dap = _need_on(dA, f32, (pool.rows, pool.k), dev, "dA")
+        dbp = _need_on(dBt, f32, (pool.rows, pool.d), dev, "dBt")
+        ws = workspace(qlora_bwd_requests_workspace_bytes(q, pool, plan), dev) if ws is None else _need_ws(ws, dev)
+        _check(lib().qlora_bwd_requests(ctypes.byref(q.cstruct), pool._ref, plan._ref, xp, up, gp, dxp, dap, dbp,
+                                        ws.data_ptr(), ws.numel(), st), "qlora_bwd_requests")
+    return dX, dA, dBt
+
+
 def lora_muon_workspace_bytes(n: int, rows: int, cols: int) -> int:
     return lib().lora_muon_workspace_bytes(n, rows, cols)
 
@@ -759,6 +832,8 @@ def lora_muon_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Ten
     n = 1 if master.dim() == 2 else master.shape[0]
     rows, cols = master.shape[-2], master.shape[-1]
     dev = master.device
+    if n == 0:
+        return
     if dev.type != "cuda":
         raise ValueError("master: must be a CUDA tensor")
     ptrs = [_need_on(t, dt, master.shape, dev, name)

@@ -2012,6 +2012,47 @@ int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const
   return requests_bwd(*pool, *req, X, U_saved, dY, base, dX, dA, dBt, w, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t qlora_fwd_requests_workspace_bytes(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req) {
+  if (!q || check_pool_shape(pool, req) != QLORA_OK || q->d != pool->d || q->k != pool->k) return 0;
+  return carve_requests_base(nullptr, *q, *pool, *req, false).bytes;
+}
+
+int qlora_fwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
+                       uint16_t* Y, float* U_save, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  QLORA_TRY(check_requests_base(q, pool, req));
+  if (req->T == 0) return QLORA_OK;
+  if (!X || !Y || !ws) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(U_save) || !aligned16(ws)) return QLORA_ERR_MISALIGNED;
+  const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, false);
+  if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  QLORA_TRY(ensure_device());
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  QLORA_TRY(requests_base(false, q, X, req->T, Y, w.scales, st));
+  return requests_fwd(*pool, *req, X, Y, Y, U_save, w.w, st);
+}
+
+size_t qlora_bwd_requests_workspace_bytes(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req) {
+  if (!q || check_pool_shape(pool, req) != QLORA_OK || q->d != pool->d || q->k != pool->k) return 0;
+  return carve_requests_base(nullptr, *q, *pool, *req, true).bytes;
+}
+
+int qlora_bwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
+                       const float* U_saved, const uint16_t* dY, uint16_t* dX, float* dA, float* dBt, void* ws,
+                       size_t ws_bytes, qlora_stream_t stream) {
+  QLORA_TRY(check_requests_base(q, pool, req));
+  if (!dA || !dBt || !ws) return QLORA_ERR_INVALID_ARG;
+  if (req->T > 0 && (!X || !U_saved || !dY || !dX)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(U_saved) || !aligned16(dY) || !aligned16(dX) || !aligned16(dA) || !aligned16(dBt) ||
+      !aligned16(ws))
+    return QLORA_ERR_MISALIGNED;
+  const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, true);
+  if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  QLORA_TRY(ensure_device());
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (req->T > 0) QLORA_TRY(requests_base(true, q, dY, req->T, dX, w.scales, st));
+  return requests_bwd(*pool, *req, X, U_saved, dY, dX, dX, dA, dBt, w.w, st);
+}
+
 size_t lora_muon_workspace_bytes(int64_t n, int64_t rows, int64_t cols) {
   if (check_muon_shape(n, rows, cols) != QLORA_OK) return 0;
   return carve_muon(nullptr, n, rows, cols).bytes;

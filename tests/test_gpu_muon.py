@@ -113,6 +113,11 @@ def test_captured_beside_another_shape():
     assert np.array_equal(d[0].double().cpu().numpy(), ref) and np.array_equal(d[1].double().cpu().numpy(), rm)
 
 
+def test_an_empty_stack_is_nothing_to_do():
+    W = torch.zeros(0, 4, 64, device="cuda")
+    q4.lora_muon_step(W, W.to(torch.bfloat16), W, W, lr=0.1)
+
+
 def test_refusals_of_the_binding():
     W = torch.zeros(4, 64, device="cuda")
     w16 = W.to(torch.bfloat16)

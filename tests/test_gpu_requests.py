@@ -164,6 +164,9 @@ def test_refusals_of_the_binding():
         q4.RequestPlan(5000, 1, 8)
     with pytest.raises(IndexError):
         b.pool.rows_of(b.n)
+    for held, name in ((b.pool, "A"), (b.pool, "scale"), (b.plan, "order")):
+        with pytest.raises(AttributeError):       # the addresses are in a C struct
+            setattr(held, name, getattr(held, name).clone())
     with pytest.raises(ValueError):
         b.pool.load(0, b.pool.A[:4], b.pool.Bt[:8].t())
 
