@@ -228,20 +228,26 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // CTA of the cluster, which adds them in rank order and writes its share of the
 // N output columns.  (The sums travel as asynchronous stores that count down
 // the receiver's barrier: no cluster-wide fence, 0.9 us less than a cluster
-// barrier and remote loads.)  One launch, the factors read once, all
-// arithmetic in fp32 on CUDA cores.
+// barrier and remote loads.)  One launch, the factors read once.
 //
 // The factors are what has to be read (a few tokens' X is nothing), so a
 // producer thread streams this CTA's part of both through a ring of TMA boxes,
-// 16 rows x 256 columns a stage: 48 KB are in flight per CTA from the first
+// 16 rows x 256 columns a stage: 40 KB are in flight per CTA from the first
 // moment, and the second factor arrives while the cluster still adds up U.
+// What is left is the time a stage takes the warps, so the products go through
+// m16n8k16 tensor instructions with the factor's rows (U) or columns (output)
+// as M and the tokens as N = 8: a tenth of the instructions of multiply-adds,
+// too small a product for tcgen05's 128 rows.  Sums over K are cut into at most
+// 32 columns a warp and stage and added in fp32; for the output, U enters as
+// two bf16 terms (2^-16, far below the one rounding of the bf16 output).
 constexpr int kFewTile = 8;
 constexpr int kFewWarps = 8;                   // consumers; one more warp produces
 constexpr int kFewThreads = 32 * (kFewWarps + 1);
 constexpr int kFewRows = 16;                   // rows of a stage
-constexpr int kFewCols = 256;                  // columns of a stage
-constexpr int kFewStages = 6;
+constexpr int kFewCols = 256;                  // columns of a stage, 32 per warp
+constexpr int kFewStages = 5;
 constexpr int kFewStageBytes = kFewRows * kFewCols * 2;
+constexpr int kFewGroup = 32;                  // rows of U whose sums are exchanged at once
 
 struct FewArgs {
   const uint16_t* X;       // T x K
@@ -255,47 +261,46 @@ struct FewArgs {
   PoolArgs pool;
 };
 
-struct FewShared {
+struct alignas(128) FewShared {
+  // [4 blocks of 64 columns][2 x 8 rows][128 bytes], 128B-swizzled
+  uint8_t ring[kFewStages * kFewStageBytes];
+  float red[kFewWarps * kFewGroup * kFewTile];   // [warp][row][token]; later [warp][token][32 columns]
   uint64_t full[kFewStages], empty[kFewStages], ready;
-  int abort_flag;
-  alignas(16) float red[kFewTile * kFewCols];    // the second half of the rows' sums
-  alignas(128) uint8_t ring[kFewStages * kFewStageBytes];
-  // behind it, by the pool's width: float u[8][width] (scaled U), then what the
-  // cluster's CTAs sent, part[CTA][row][tokens of the tile, a power of two]
-  __device__ __forceinline__ float* u() { return reinterpret_cast<float*>(ring + kFewStages * kFewStageBytes); }
-  __device__ __forceinline__ float* part(int width) { return u() + kFewTile * width; }
+  int abort_flag, unused[3];
+  // behind it, by the pool's width: what the cluster's CTAs sent, float
+  // part[CTA][row][token], then scaled U as bf16 [hi, mid][token][width + 8]
+  __device__ __forceinline__ float* part() { return reinterpret_cast<float*>(this + 1); }
+  __device__ __forceinline__ uint16_t* u(int width, int csize) {
+    return reinterpret_cast<uint16_t*>(part() + csize * width * kFewTile);
+  }
 };
 __host__ __device__ __forceinline__ size_t few_smem_bytes(int width, int csize) {
-  return sizeof(FewShared) + (size_t)(1 + csize) * kFewTile * width * 4;
+  return 1024 + sizeof(FewShared) + (size_t)csize * kFewTile * width * 4 + (size_t)2 * kFewTile * (width + 8) * 2;
 }
 
-// N floats to shared memory of a CTA of the cluster, counted on its barrier.
-template <int N>
-__device__ __forceinline__ void store_async(uint32_t cluster_addr, const float* v, uint32_t cluster_bar) {
-  if (N == 1)
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
-                 "r"(__float_as_uint(v[0])), "r"(cluster_bar)
-                 : "memory");
-  else if (N == 2)
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(cluster_addr),
-                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(cluster_bar)
-                 : "memory");
-  else
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                       cluster_addr + 4u * i),
-                   "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), "r"(__float_as_uint(v[i + 2])),
-                   "r"(__float_as_uint(v[i + 3])), "r"(cluster_bar)
-                   : "memory");
+// Four floats to shared memory of another CTA of the cluster, counted on its barrier.
+__device__ __forceinline__ void store_async4(uint32_t cluster_addr, float4 v, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   cluster_addr),
+               "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)),
+               "r"(cluster_bar)
+               : "memory");
+}
+// d += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
 }
 
-// Two products and sums at once: d.{lo,hi} += a.{lo,hi} * b.{lo,hi}.
-__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
-  uint64_t x = *reinterpret_cast<uint64_t*>(&d);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(x) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  d = *reinterpret_cast<float2*>(&x);
-}
+static_assert(sizeof(FewShared) % 128 == 0, "what lies behind it is read in 16-byte words");
 
 struct FewRing {
   int at = 0;
@@ -310,19 +315,21 @@ struct FewRing {
 
 // Stages of one factor for this CTA (one thread): for the first factor all
 // columns of 16 rows, then the next rows; for the second all rows of 256
-// columns.  Boxes of 8 rows: a stage's second one only where the rank has it.
-__device__ __forceinline__ bool few_produce(FewShared& s, FewRing& ring, int& issued, const CUtensorMap* w, int first, int rank,
-                                            int c0, int c1, bool rows_first) {
+// columns.  Boxes of 64 columns x 16 rows, or 8 where the rank ends in a
+// stage's first 8; columns only up to the share's end.
+__device__ __forceinline__ bool few_produce(FewShared& s, FewRing& ring, int& issued, const CUtensorMap* w8,
+                                            const CUtensorMap* w16, int first, int rank, int c0, int c1, bool rows_first) {
   const int rb = (rank + kFewRows - 1) / kFewRows, cb = (c1 - c0 + kFewCols - 1) / kFewCols;
   for (int i = 0; i < rb * cb; ++i) {
     const int r = (rows_first ? i % rb : i / cb) * kFewRows, c = c0 + (rows_first ? i / rb : i % cb) * kFewCols;
     const bool two = rank - r > 8;
+    const int blocks = min(4, (c1 - c + 63) / 64);
     const uint32_t full = smem_u32(&s.full[ring.at]);
     if (!mbar_wait_bounded(smem_u32(&s.empty[ring.at]), ring.phase ^ 1u, &s.abort_flag)) return false;
-    mbar_arrive_expect_tx(full, two ? kFewStageBytes : kFewStageBytes / 2);
+    mbar_arrive_expect_tx(full, (uint32_t)(blocks * (two ? 2048 : 1024)));
     const uint32_t dst = smem_u32(s.ring) + (uint32_t)(ring.at * kFewStageBytes);
-    tma_load_2d(dst, w, full, c, first + r);
-    if (two) tma_load_2d(dst + kFewStageBytes / 2, w, full, c, first + r + 8);
+    const CUtensorMap* w = two ? w16 : w8;
+    for (int b = 0; b < blocks; ++b) tma_load_2d(dst + b * 2048u, w, full, c + 64 * b, first + r);
     ring.next();
     ++issued;
   }
@@ -330,166 +337,165 @@ __device__ __forceinline__ bool few_produce(FewShared& s, FewRing& ring, int& is
 }
 
 // The consumers' side of a tile (warps 0 .. 7).  X's values stay in L1.
-template <int NT>
-__device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, const AdapterRows& ad, const int (&tok)[kFewTile],
-                                            int count, int q, int k0, int k1, int n0, int n1) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rb = (ad.rank + kFewRows - 1) / kFewRows;
-  float* s_u = s.u();
-  float* s_part = s.part(p.width);
+__device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, const AdapterRows& ad, const int4& tile, int count,
+                                            int q, int k0, int k1, int n0, int n1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
+  float* s_part = s.part();
+  uint16_t* s_u = s.u(p.width, p.csize);
+  const int upitch = p.width + 8;                // bf16 values; rows of U in distinct banks
+  const int quads = count <= 4 ? 1 : 2;          // fours of tokens in use
   if (p.csize > 1 && threadIdx.x == 0)
-    mbar_arrive_expect_tx(smem_u32(&s.ready), (uint32_t)((p.csize - 1) * ad.rank * NT * 4));
+    mbar_arrive_expect_tx(smem_u32(&s.ready), (uint32_t)((p.csize - 1) * ad.rank * quads * 16));
+  const int tokn = p.order[tile.y + min(hi, count - 1)];      // the token of this lane's column
+  const uint16_t* xrow = p.X + (int64_t)tokn * p.K;
   FewRing ring;
   bool ok = true;
-  // U: a warp takes rows w and w + 8 of a stage, a lane 8 columns
-  for (int r = 0; r < ad.rank && ok; r += kFewRows) {
-    float2 acc[2][NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[0][t] = acc[1][t] = make_float2(0.f, 0.f);
-    for (int c = k0; c < k1; c += kFewCols) {
-      const int x0 = c + lane * 8;
-      const bool in = x0 < k1;
-      uint4 xv[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        xv[t] = in ? __ldg(reinterpret_cast<const uint4*>(p.X + (int64_t)tok[t] * p.K + x0)) : make_uint4(0, 0, 0, 0);
-      ok = mbar_wait_bounded(smem_u32(&s.full[ring.at]), ring.phase, &s.abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-      const uint8_t* st = s.ring + ring.at * kFewStageBytes + warp * (kFewCols * 2) + lane * 16;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (in && r + warp + 8 * i < ad.rank) {
-          const uint4 w = *reinterpret_cast<const uint4*>(st + i * 8 * kFewCols * 2);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 wf = make_float2(bf_lo(ws[j]), bf_hi(ws[j]));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint32_t xs[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
-              fma2(acc[i][t], wf, make_float2(bf_lo(xs[j]), bf_hi(xs[j])));
-            }
-          }
+  // U: a warp takes 32 columns of a stage; a lane's 8 consecutive columns are
+  // the 4 values of two k-steps (any order of the columns gives the same sum)
+  const uint32_t a_off = (uint32_t)((warp >> 1) * 2048 + hi * 128 + ((((warp & 1) * 4 + lo) ^ hi) << 4));
+  for (int g = 0; g < ad.rank; g += kFewGroup) {
+    for (int r = g; r < min(ad.rank, g + kFewGroup) && ok; r += kFewRows) {
+      const bool two = ad.rank - r > 8;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int c = k0; c < k1; c += kFewCols) {
+        const int x0 = c + warp * 32 + lo * 8;
+        const uint4 x = x0 < k1 ? __ldg(reinterpret_cast<const uint4*>(xrow + x0)) : make_uint4(0, 0, 0, 0);
+        ok = mbar_wait_bounded(smem_u32(&s.full[ring.at]), ring.phase, &s.abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (c + (warp >> 1) * 64 < k1) {         // (a block behind the share's end is not loaded)
+          const uint8_t* st = s.ring + ring.at * kFewStageBytes + a_off;
+          const uint4 w0 = *reinterpret_cast<const uint4*>(st);
+          const uint4 w1 = two ? *reinterpret_cast<const uint4*>(st + 1024) : make_uint4(0, 0, 0, 0);
+          mma16816(acc, w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+          mma16816(acc, w0.z, w1.z, w0.w, w1.w, x.z, x.w);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
+        ring.next();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
-      ring.next();
+      float* red = s.red + (warp * kFewGroup + (r - g) + hi) * kFewTile + 2 * lo;
+      *reinterpret_cast<float2*>(red) = make_float2(acc[0], acc[1]);
+      *reinterpret_cast<float2*>(red + 8 * kFewTile) = make_float2(acc[2], acc[3]);
     }
+    named_bar_sync(1, 32 * kFewWarps);
+    // the warps' sums of four tokens of a row, added in order, to every CTA
+    const int rows = min(kFewGroup, ad.rank - g);
+    if ((int)threadIdx.x < rows * quads) {
+      const int i = threadIdx.x / quads, t = threadIdx.x % quads * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = r + warp + 8 * i;
-      if (row >= ad.rank) break;
-      float v[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        v[t] = acc[i][t].x + acc[i][t].y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[t] += __shfl_xor_sync(0xFFFFFFFFu, v[t], o);
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float4 f = *reinterpret_cast<const float4*>(s.red + (w * kFewGroup + i) * kFewTile + t);
+        v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
       }
-      // lane c sends the row's sums to CTA c, this CTA's own are plain stores
-      if (lane == q) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s_part[(q * p.width + row) * NT + t] = v[t];
-      } else if (lane < p.csize)
-        store_async<NT>(mapa_shared(smem_u32(s_part + (q * p.width + row) * NT), (uint32_t)lane), v,
-                        mapa_shared(smem_u32(&s.ready), (uint32_t)lane));
-      __syncwarp();
+      float* at = s_part + (q * p.width + g + i) * kFewTile + t;
+      *reinterpret_cast<float4*>(at) = v;
+      const uint32_t a = smem_u32(at), bar = smem_u32(&s.ready);
+      for (int c = 1; c < p.csize; ++c) {
+        const uint32_t to = (uint32_t)((q + c) & (p.csize - 1));
+        store_async4(mapa_shared(a, to), v, mapa_shared(bar, to));
+      }
     }
+    named_bar_sync(1, 32 * kFewWarps);
   }
-  // base comes in while the cluster meets
-  const int g = threadIdx.x >> 7, x2 = (threadIdx.x & 127) * 2;     // half of a stage's rows, 2 columns
-  uint32_t base[NT];
+  // base comes in while the cluster's sums do: lane: token pair half, 2 columns
+  const int th = lane >> 4, x2 = warp * 32 + (lane & 15) * 2;
+  int tokb[4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-    base[t] = g == 0 && p.base && t < count && n0 + x2 < n1
-                  ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tok[t] * p.N + n0 + x2) : 0u;
-  named_bar_sync(1, 32 * kFewWarps);
+  for (int i = 0; i < 4; ++i) tokb[i] = __shfl_sync(0xFFFFFFFFu, tokn, (2 * i + th) * 4);
+  uint32_t ahead[4];                             // base's values of the next 256 columns
+  auto load_base = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ahead[i] = p.base && 2 * i + th < count && c + x2 < n1
+                     ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tokb[i] * p.N + c + x2) : 0u;
+  };
+  load_base(n0);
   if (p.csize > 1) ok = mbar_wait_bounded(smem_u32(&s.ready), 0, &s.abort_flag) && ok;
   __syncwarp();
-  for (int e = threadIdx.x; e < ad.rank * NT; e += 32 * kFewWarps) {
-    const int r = e / NT, t = e % NT;
-    float v = 0.f;
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  const int r16 = (ad.rank + 15) & ~15;
+  for (int e = threadIdx.x; e < r16 * kFewTile; e += 32 * kFewWarps) {
+    const int r = e / kFewTile, t = e % kFewTile;
+    float v = 0.f;                               // rows behind the rank and tokens behind the tile's count for nothing
+    if (r < ad.rank && t < count) {
 #pragma unroll 8
-    for (int c = 0; c < p.csize; ++c) v += s_part[(c * p.width + r) * NT + t];
-    s_u[t * p.width + r] = ad.scale * v;
-    if (q == 0 && t < count) {
-      if (p.U) p.U[(int64_t)tok[t] * p.width + r] = v;
-      if (p.sU) p.sU[(int64_t)tok[t] * p.width + r] = ad.scale * v;
+      for (int c = 0; c < p.csize; ++c) v += s_part[(c * p.width + r) * kFewTile + t];
+      if (q == 0) {
+        const int64_t at = (int64_t)p.order[tile.y + t] * p.width + r;
+        if (p.U) p.U[at] = v;
+        if (p.sU) p.sU[at] = ad.scale * v;
+      }
+      v *= ad.scale;
     }
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    const __nv_bfloat16 m = __float2bfloat16_rn(v - __bfloat162float(h));
+    s_u[t * upitch + r] = *reinterpret_cast<const uint16_t*>(&h);
+    s_u[(kFewTile + t) * upitch + r] = *reinterpret_cast<const uint16_t*>(&m);
   }
-  // rows up to the stage's 16 multiply whatever the stage holds: make that nothing
-  for (int e = threadIdx.x; e < (rb * kFewRows - ad.rank) * NT; e += 32 * kFewWarps)
-    s_u[(e % NT) * p.width + ad.rank + e / NT] = 0.f;
   named_bar_sync(1, 32 * kFewWarps);
+  // output: a warp's 32 columns are two M of 16 (transposed fragments), the rows K
+  const int lr = (lane & 7) + ((lane >> 4) << 3), lj = ((lane >> 3) & 1) * 8;   // this lane's row and column of a 16 x 16 block
   for (int c = n0; c < n1; c += kFewCols) {
-    const int x = c + x2;
-    const bool in = x < n1;
-    if (c > n0) {
+    uint32_t base[4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        base[t] = g == 0 && p.base && t < count && in ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tok[t] * p.N + x) : 0u;
-    }
-    float acc[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
+    for (int i = 0; i < 4; ++i) base[i] = ahead[i];
+    load_base(c + kFewCols);
+    float acc[2][4] = {};
     for (int r = 0; r < ad.rank && ok; r += kFewRows) {
       ok = mbar_wait_bounded(smem_u32(&s.full[ring.at]), ring.phase, &s.abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-      if (in && r + 8 * g < ad.rank) {
-        const uint8_t* st = s.ring + ring.at * kFewStageBytes + 8 * g * (kFewCols * 2) + x2 * 2;
-        const int m = min(8, ad.rank - r - 8 * g);
-        uint32_t w[8];
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (c + (warp >> 1) * 64 < n1) {
+        const bool two = ad.rank - r > 8;
+        const uint16_t* u = s_u + hi * upitch + r + 2 * lo;
+        const uint32_t h0 = *reinterpret_cast<const uint32_t*>(u), h1 = *reinterpret_cast<const uint32_t*>(u + 8);
+        const uint32_t m0 = *reinterpret_cast<const uint32_t*>(u + kFewTile * upitch);
+        const uint32_t m1 = *reinterpret_cast<const uint32_t*>(u + kFewTile * upitch + 8);
+        const uint32_t st = smem_u32(s.ring) + (uint32_t)(ring.at * kFewStageBytes + (warp >> 1) * 2048 + (lr >> 3) * 1024 + (lr & 7) * 128);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < m ? *reinterpret_cast<const uint32_t*>(st + i * kFewCols * 2) : 0u;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float4 a = *reinterpret_cast<const float4*>(s_u + t * p.width + r + 8 * g);
-          const float4 b = *reinterpret_cast<const float4*>(s_u + t * p.width + r + 8 * g + 4);
-          const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[t][0] = __fmaf_rn(u[i], bf_lo(w[i]), acc[t][0]);
-            acc[t][1] = __fmaf_rn(u[i], bf_hi(w[i]), acc[t][1]);
-          }
+        for (int j = 0; j < 2; ++j) {
+          uint32_t a[4];
+          ldmatrix4_trans(a, st + (uint32_t)((((warp & 1) * 4 + 2 * j + (lj >> 3)) ^ (lr & 7)) << 4));
+          if (!two) a[2] = a[3] = 0u;            // (rows that were not loaded)
+          mma16816(acc[j], a[0], a[1], a[2], a[3], h0, h1);
+          mma16816(acc[j], a[0], a[1], a[2], a[3], m0, m1);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
       ring.next();
     }
-    if (rb * kFewRows > 8 && ad.rank > 8) {      // the second half's sums
-      named_bar_sync(1, 32 * kFewWarps);
-      if (g == 1) {
+    // [token][column] of this warp, then rows of 64 bytes
+    float* tr = s.red + warp * (kFewTile * 32);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<float2*>(s.red + t * kFewCols + x2) = make_float2(acc[t][0], acc[t][1]);
-      }
-      named_bar_sync(1, 32 * kFewWarps);
-      if (g == 0) {
+    for (int j = 0; j < 2; ++j) {
+      tr[(2 * lo) * 32 + 16 * j + hi] = acc[j][0];
+      tr[(2 * lo + 1) * 32 + 16 * j + hi] = acc[j][1];
+      tr[(2 * lo) * 32 + 16 * j + hi + 8] = acc[j][2];
+      tr[(2 * lo + 1) * 32 + 16 * j + hi + 8] = acc[j][3];
+    }
+    __syncwarp();
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float2 v = *reinterpret_cast<const float2*>(s.red + t * kFewCols + x2);
-          acc[t][0] += v.x;
-          acc[t][1] += v.y;
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = *reinterpret_cast<const float2*>(tr + (2 * i + th) * 32 + (lane & 15) * 2);
+      if (2 * i + th < count && c + x2 < n1) {
+        const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(base[i]) + v.x, bf_hi(base[i]) + v.y);
+        *reinterpret_cast<uint32_t*>(p.out + (int64_t)tokb[i] * p.N + c + x2) = *reinterpret_cast<const uint32_t*>(&o);
       }
     }
-    if (g == 0 && in) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t >= count) break;
-        const __nv_bfloat162 o = __floats2bfloat162_rn(bf_lo(base[t]) + acc[t][0], bf_hi(base[t]) + acc[t][1]);
-        *reinterpret_cast<uint32_t*>(p.out + (int64_t)tok[t] * p.N + x) = *reinterpret_cast<const uint32_t*>(&o);
-      }
-    }
+    __syncwarp();
   }
 }
 
-__global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __grid_constant__ CUtensorMap w1,
-                                                                      const __grid_constant__ CUtensorMap w2,
+__global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __grid_constant__ CUtensorMap w1a,
+                                                                      const __grid_constant__ CUtensorMap w1b,
+                                                                      const __grid_constant__ CUtensorMap w2a,
+                                                                      const __grid_constant__ CUtensorMap w2b,
                                                                       const __grid_constant__ FewArgs p) {
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  FewShared& s = *reinterpret_cast<FewShared*>(smem_raw);
+  extern __shared__ uint8_t smem_raw[];
+  FewShared& s = *reinterpret_cast<FewShared*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int csize = p.csize;                   // CTAs of a cluster
   const int q = (int)(blockIdx.x % csize);
   if (threadIdx.x == 0) {
@@ -500,16 +506,16 @@ __global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __gr
     mbar_init(smem_u32(&s.ready), 1);
     s.abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&w1b);
+    tma_prefetch_desc(&w2b);
   }
+  __syncwarp();
   cluster_sync();                              // every CTA's barriers are set up
   griddep_wait();
   griddep_launch_dependents();
   const int4 tile = p.tiles[blockIdx.x / csize];
   if (tile.z <= 0) return;                     // the whole cluster leaves
   const int count = min(tile.z, kFewTile);
-  int tok[kFewTile];
-#pragma unroll
-  for (int t = 0; t < kFewTile; ++t) tok[t] = p.order[tile.y + min(t, count - 1)];
   const AdapterRows ad = adapter_rows(p.pool, tile.x, p.width);
   // columns of U beyond the rank are zero
   if (q == 0 && (p.U || p.sU)) {
@@ -542,17 +548,13 @@ __global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __gr
     if ((threadIdx.x & 31) == 0) {
       FewRing ring;
       int issued = 0;
-      if (!few_produce(s, ring, issued, &w1, ad.first, ad.rank, k0, k1, false) ||
-          !few_produce(s, ring, issued, &w2, ad.first, ad.rank, n0, n1, true))
+      if (!few_produce(s, ring, issued, &w1a, &w1b, ad.first, ad.rank, k0, k1, false) ||
+          !few_produce(s, ring, issued, &w2a, &w2b, ad.first, ad.rank, n0, n1, true))
         for (int i = 0; i < min(issued, kFewStages); ++i)        // let copies in flight land
           mbar_wait_bounded(smem_u32(&s.full[i]), (uint32_t)((issued - 1 - i) / kFewStages & 1), nullptr);
     }
-    __syncwarp();
   } else {
-    if (count == 1) few_consume<1>(p, s, ad, tok, count, q, k0, k1, n0, n1);
-    else if (count == 2) few_consume<2>(p, s, ad, tok, count, q, k0, k1, n0, n1);
-    else if (count <= 4) few_consume<4>(p, s, ad, tok, count, q, k0, k1, n0, n1);
-    else few_consume<8>(p, s, ad, tok, count, q, k0, k1, n0, n1);
+    few_consume(p, s, ad, tile, count, q, k0, k1, n0, n1);
   }
   __syncwarp();
   cluster_sync();                              // no CTA leaves while another may still send to it
