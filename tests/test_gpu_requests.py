@@ -29,6 +29,9 @@ CASES = {
     "empty requests only": dict(k=64, d=64, ranks=[8], lens=[0, 0], ids=[0, 0], T=5),
     "no requests": dict(k=64, d=64, ranks=[8], lens=[], ids=[], T=5),
     "one more than few tokens": dict(k=520, d=512, ranks=[20, 9], lens=[100, 29], ids=[1, 0]),
+    "decoding, many": dict(k=512, d=1032, ranks=[8, 24, 64] * 40, lens=[1] * 300, ids=[(7 * i) % 121 - 1 for i in range(300)],
+                           T=311),
+    "decoding, more than tokens for it": dict(k=136, d=72, ranks=[8, 24], lens=[1] * 1030, ids=[i % 3 - 1 for i in range(1030)]),
     "tiles end inside": dict(k=320, d=192, ranks=[16, 40, 7], lens=[127, 1, 128, 129, 8, 7, 9],
                              ids=[0, 1, 1, 2, 0, 2, 1]),
     "rank 256": dict(k=200, d=328, ranks=[256, 17], lens=[70, 65, 30], ids=[0, 1, 0]),
