@@ -566,6 +566,7 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const MuonArgs p) {
   const double* part = p.part + mat * p.chunks * sq;
   double t = 0.0;
   for (int i = threadIdx.x; i < p.r; i += 256)
+#pragma unroll 8
     for (int c = 0; c < p.chunks; ++c) t += part[c * sq + (int64_t)i * p.rp + i];
   s_sum[threadIdx.x] = t;
   __syncthreads();
@@ -576,52 +577,65 @@ __global__ void __launch_bounds__(256) muon_norm_kernel(const MuonArgs p) {
   const double f = sqrt(s_sum[0]) + p.eps, inv = 1.0 / f;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < sq; e += (int64_t)gridDim.x * 256) {
     double v = 0.0;
+#pragma unroll 8
     for (int c = 0; c < p.chunks; ++c) v += part[c * sq + e];
     p.R[mat * sq + e] = v * inv * inv;
     p.P[mat * sq + e] = (e / p.rp == e % p.rp) ? inv : 0.0;   // P carries the norm of x0 = u inv
   }
 }
 
-// One 32 x 32 block of an r x r product; what: 0: Q = a I + b R + c R R,
-// 1: H = Q R (z < n) and the next P = Q P (z >= n, into `out2`), 2: R = Q H.
-__global__ void __launch_bounds__(256) muon_square_kernel(const MuonArgs p, int what, const double* pin, double* pout, int n) {
-  __shared__ double s_a[32][33];
-  __shared__ double s_b[32][33];
+// One 8 x 8 block per warp of an r x r product; what: 0: Q = a I + b R + c R R,
+// 1: H = Q R (y < n) and the next P = Q P (y >= n, into `pout`), 2: R = Q H.
+// All factors are symmetric, so both operands are rows: a lane loads 16-byte
+// words (two k-steps, in any order), 128 of the inner sum in flight at once, and
+// nothing is staged.  Bound by the latency of one round of loads per launch.
+constexpr int kSquareThreads = 128;
+__device__ __forceinline__ double2 load_ahead(const double2* p) {
+  double2 v;
+  asm volatile("ld.global.cg.v2.f64 {%0, %1}, [%2];" : "=d"(v.x), "=d"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__global__ void __launch_bounds__(kSquareThreads, 1) muon_square_kernel(const MuonArgs p, int what, const double* pin, double* pout,
+                                                                     int n) {
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t sq = (int64_t)p.rp * p.rp;
-  const bool second = (int)blockIdx.z >= n;
-  const int64_t mat = second ? blockIdx.z - n : blockIdx.z;
+  const bool second = (int)blockIdx.y >= n;
+  const int64_t mat = second ? blockIdx.y - n : blockIdx.y;
   const double* A = (what == 0 ? p.R : p.Q) + mat * sq;
   const double* B = (what == 0 ? p.R : what == 2 ? p.H : second ? pin : p.R) + mat * sq;
   double* O = (what == 0 ? p.Q : what == 2 ? p.R : second ? pout : p.H) + mat * sq;
-  const int i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
-  const int ti = threadIdx.x / 16 * 2, tj = threadIdx.x % 16 * 2;
-  double acc[2][2] = {};
-  for (int kb = 0; kb < p.rp; kb += 32) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < 1024; e += 256) {
-      const int x = e / 32, y = e % 32;
-      s_a[x][y] = (i0 + x < p.rp && kb + y < p.rp) ? A[(int64_t)(i0 + x) * p.rp + kb + y] : 0.0;
-      s_b[x][y] = (kb + x < p.rp && j0 + y < p.rp) ? B[(int64_t)(kb + x) * p.rp + j0 + y] : 0.0;
+  const int blocks = p.rp / 8, block = blockIdx.x * (kSquareThreads / 32) + (threadIdx.x >> 5);
+  if (block >= blocks * blocks) return;
+  const int lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
+  const int i0 = block / blocks * 8, j0 = block % blocks * 8;
+  const double2* a = reinterpret_cast<const double2*>(A + (int64_t)(i0 + hi) * p.rp) + lo;
+  const double2* b = reinterpret_cast<const double2*>(B + (int64_t)(j0 + hi) * p.rp) + lo;
+  double d[2] = {0.0, 0.0}, e[2] = {0.0, 0.0};
+  for (int k = 0; k < p.rp; k += 128) {
+    double2 x[16], y[16];
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      const bool in = k + 8 * s < p.rp;
+      x[s] = in ? load_ahead(a + k / 2 + 4 * s) : make_double2(0.0, 0.0);
+      y[s] = in ? load_ahead(b + k / 2 + 4 * s) : make_double2(0.0, 0.0);
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+    for (int s = 0; s < 16; ++s)                 // (keeps the loads in front of the first product)
+      asm volatile("" : "+d"(x[s].x), "+d"(x[s].y), "+d"(y[s].x), "+d"(y[s].y));
 #pragma unroll
-        for (int w = 0; w < 2; ++w) acc[q][w] = fma(s_a[ti + q][k], s_b[k][tj + w], acc[q][w]);
+    for (int s = 0; s < 16; ++s) {
+      dmma(d, x[s].x, y[s].x);
+      dmma(e, x[s].y, y[s].y);
+    }
   }
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int i = i0 + ti + q, j = j0 + tj + w;
-      if (i >= p.rp || j >= p.rp) continue;
-      double v = acc[q][w];
-      if (what == 0) v = p.c * v + p.b * A[(int64_t)i * p.rp + j] + (i == j ? p.a : 0.0);
-      O[(int64_t)i * p.rp + j] = v;
-    }
+  for (int w = 0; w < 2; ++w) {
+    const int i = i0 + hi, j = j0 + 2 * lo + w;
+    double v = d[w] + e[w];
+    if (what == 0) v = p.c * v + p.b * A[(int64_t)i * p.rp + j] + (i == j ? p.a : 0.0);
+    O[(int64_t)i * p.rp + j] = v;
+  }
 }
 
 // x = P u for 64 short-side rows and 32 long-side elements, and the update of
