@@ -108,7 +108,7 @@ struct Gram64 {
   static constexpr int kSmem = kGram64Threads / 32 * kTiles * 64 * 8;
 };
 template <int NB, bool kTall>
-__global__ void __launch_bounds__(kGram64Threads) muon_gram64_kernel(const MuonArgs p, int csize) {
+__global__ void __launch_bounds__(kGram64Threads, 1) muon_gram64_kernel(const MuonArgs p, int csize) {
   constexpr int kTiles = Gram64<NB>::kTiles, kWarps = kGram64Threads / 32;
   extern __shared__ __align__(16) double s_acc[];          // [warp][tile * 64]
   griddep_wait();
@@ -254,7 +254,7 @@ __device__ __forceinline__ void poly_spread(double* at, const double (&d)[2], in
   }
 }
 template <int NB, bool kTall>
-__global__ void __launch_bounds__(Poly64<NB>::kThreads) muon_poly64_kernel(const MuonArgs p, int parts, int steps) {
+__global__ void __launch_bounds__(Poly64<NB>::kThreads, 1) muon_poly64_kernel(const MuonArgs p, int parts, int steps) {
   using C = Poly64<NB>;
   constexpr int kTiles = Gram64<NB>::kTiles, kMat = C::kRp * C::kPitch;
   constexpr uint32_t kOthers = (NB - 1) * 8 * C::kRp * 8;  // bytes that the other CTAs send per exchange
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(Poly64<NB>::kThreads) muon_poly64_kernel(const
 // is chosen so that every lane reads and writes runs of consecutive floats.
 constexpr int kApply64Threads = 128;
 template <int NB, bool kTall>
-__global__ void __launch_bounds__(kApply64Threads) muon_apply64_kernel(const MuonArgs p) {
+__global__ void __launch_bounds__(kApply64Threads, 2) muon_apply64_kernel(const MuonArgs p) {
   constexpr int kRp = 8 * NB, kPitch = kRp + 4, KS = 2 * NB;
   __shared__ __align__(16) double s_p[kRp * kPitch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(float* __restrict__ 
 constexpr int kGramThreads = 256;
 constexpr int kGramStep = 32;
 constexpr int kGramPitch = 66;             // doubles per staged long-side element
-__global__ void __launch_bounds__(kGramThreads) muon_gram_kernel(const MuonArgs p) {
+__global__ void __launch_bounds__(kGramThreads, 2) muon_gram_kernel(const MuonArgs p) {
   __shared__ __align__(16) double s_i[kGramStep][kGramPitch];
   __shared__ __align__(16) double s_j[kGramStep][kGramPitch];
   griddep_wait();
@@ -513,22 +513,38 @@ __global__ void __launch_bounds__(kGramThreads) muon_gram_kernel(const MuonArgs 
   const int64_t mat = blockIdx.z;
   const int64_t c0 = (int64_t)blockIdx.x * p.chunk, c1 = min(p.len, c0 + p.chunk);
   const int ti = (threadIdx.x / 16) * 4, tj = (threadIdx.x % 16) * 4;
+  const int sides = bi == bj ? 1 : 2;
+  // a thread's elements of the next step are on their way while this one is multiplied
+  constexpr int kEach = 64 * kGramStep / kGramThreads;
+  float pg[2][kEach], pm[2][kEach];
+  auto fetch = [&](int64_t cb) {
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int x = 0; x < kEach; ++x) {
+        const int e = threadIdx.x + x * kGramThreads, base = (side ? bj : bi) * 64;
+        const int i = p.tall ? e % 64 : e / kGramStep, c = p.tall ? e / 64 : e % kGramStep;
+        pg[side][x] = pm[side][x] = 0.f;
+        if (side < sides && base + i < p.r && cb + c < c1) {
+          const int64_t at = muon_at(p, mat, base + i, cb + c);
+          pg[side][x] = __ldg(p.g + at);
+          pm[side][x] = __ldcg(p.m + at);
+        }
+      }
+  };
   double acc[4][4] = {};
+  fetch(c0);
   for (int64_t cb = c0; cb < c1; cb += kGramStep) {
     __syncthreads();
-    for (int side = 0; side < (bi == bj ? 1 : 2); ++side) {
-      double(*s)[kGramPitch] = side ? s_j : s_i;
-      const int base = (side ? bj : bi) * 64;
-      for (int e = threadIdx.x; e < 64 * kGramStep; e += kGramThreads) {
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int x = 0; x < kEach; ++x) {
+        const int e = threadIdx.x + x * kGramThreads;
         const int i = p.tall ? e % 64 : e / kGramStep, c = p.tall ? e / 64 : e % kGramStep;
-        double v = 0.0;
-        if (base + i < p.r && cb + c < c1) {
-          const int64_t at = muon_at(p, mat, base + i, cb + c);
-          v = (double)muon_u(p, p.g[at], p.m[at]);
-        }
-        s[c][i] = v;
+        if (side < sides) (side ? s_j : s_i)[c][i] = (double)muon_u(p, pg[side][x], pm[side][x]);
       }
-    }
+    if (cb + kGramStep < c1) fetch(cb + kGramStep);
     __syncthreads();
     const double(*sj)[kGramPitch] = bi == bj ? s_i : s_j;
 #pragma unroll 4
@@ -558,27 +574,34 @@ __global__ void __launch_bounds__(kGramThreads) muon_gram_kernel(const MuonArgs 
     }
 }
 
-// R0 = (sum of the partials in chunk order) / (|u|_F + eps)^2; P starts as I.
-__global__ void __launch_bounds__(256) muon_norm_kernel(const MuonArgs p) {
+// R0 = (sum of the partials) / (|u|_F + eps)^2; P starts as I.  Four threads per
+// element take every fourth partial each, added in a fixed order.
+__global__ void __launch_bounds__(256, 1) muon_norm_kernel(const MuonArgs p) {
   __shared__ double s_sum[256];
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t mat = blockIdx.y, sq = (int64_t)p.rp * p.rp;
   const double* part = p.part + mat * p.chunks * sq;
-  double t = 0.0;
-  for (int i = threadIdx.x; i < p.r; i += 256)
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const int64_t e = (int64_t)blockIdx.x * 64 + x;
+  double v = 0.0;
 #pragma unroll 8
-    for (int c = 0; c < p.chunks; ++c) t += part[c * sq + (int64_t)i * p.rp + i];
+  for (int c = y; c < p.chunks; c += 4) v += part[c * sq + e];
+  double t = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < p.r * p.chunks; i += 256) t += part[i / p.r * sq + (int64_t)(i % p.r) * (p.rp + 1)];
   s_sum[threadIdx.x] = t;
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
     if (threadIdx.x < o) s_sum[threadIdx.x] += s_sum[threadIdx.x + o];
     __syncthreads();
   }
-  const double f = sqrt(s_sum[0]) + p.eps, inv = 1.0 / f;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < sq; e += (int64_t)gridDim.x * 256) {
-    double v = 0.0;
-#pragma unroll 8
-    for (int c = 0; c < p.chunks; ++c) v += part[c * sq + e];
+  const double inv = 1.0 / (sqrt(s_sum[0]) + p.eps);
+  __syncthreads();
+  s_sum[threadIdx.x] = v;
+  __syncthreads();
+  if (y == 0) {
+    v = (s_sum[x] + s_sum[x + 64]) + (s_sum[x + 128] + s_sum[x + 192]);
     p.R[mat * sq + e] = v * inv * inv;
     p.P[mat * sq + e] = (e / p.rp == e % p.rp) ? inv : 0.0;   // P carries the norm of x0 = u inv
   }
@@ -638,53 +661,115 @@ __global__ void __launch_bounds__(kSquareThreads, 1) muon_square_kernel(const Mu
   }
 }
 
-// x = P u for 64 short-side rows and 32 long-side elements, and the update of
-// the master and of its 16-bit copy.
-__global__ void __launch_bounds__(256) muon_apply_kernel(const MuonArgs p, const double* P) {
-  __shared__ double s_p[64][33];           // P[i0 + i][kb + k]
-  __shared__ double s_u[32][33];           // u[kb + k][c0 + c]
+// x = P u and the update for 64 short-side rows (blockIdx.y) and 16 long-side
+// elements a warp: muon_apply64_kernel's fragments, the inner sum in parts of 64
+// with that part of P in shared memory.
+template <bool kTall>
+__global__ void __launch_bounds__(kApply64Threads, 2) muon_apply_kernel(const MuonArgs p, const double* P) {
+  constexpr int kPitch = 68, KS = 16;
+  __shared__ __align__(16) double s_p[64 * kPitch];
   griddep_wait();
-  const int64_t mat = blockIdx.z, sq = (int64_t)p.rp * p.rp;
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
+  const int64_t mat = blockIdx.z, base = mat * (int64_t)p.r * p.len, sq = (int64_t)p.rp * p.rp;
   const int i0 = blockIdx.y * 64;
-  const int64_t c0 = (int64_t)blockIdx.x * 32;
-  const int ti = threadIdx.x / 16 * 4, tc = threadIdx.x % 16 * 2;
-  double acc[4][2] = {};
-  for (int kb = 0; kb < p.r; kb += 32) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-      const int i = e / 32, k = e % 32;
-      s_p[i][k] = (i0 + i < p.rp && kb + k < p.rp) ? P[mat * sq + (int64_t)(i0 + i) * p.rp + kb + k] : 0.0;
-    }
-    for (int e = threadIdx.x; e < 32 * 32; e += 256) {
-      const int k = p.tall ? e % 32 : e / 32, c = p.tall ? e / 32 : e % 32;
-      double v = 0.0;
-      if (kb + k < p.r && c0 + c < p.len) {
-        const int64_t at = muon_at(p, mat, kb + k, c0 + c);
-        v = (double)muon_u(p, p.g[at], p.m[at]);
+  const bool vec = kTall ? (p.r & 3) == 0 : (p.len & 1) == 0;
+  const int64_t c0 = ((int64_t)blockIdx.x * 4 + warp) * 16;
+  double d[8][2][2] = {};                          // [8 rows][8 long-side elements][2]
+  for (int k0 = 0; k0 < p.rp; k0 += 64) {
+    double f[2][KS];
+    if (!kTall) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int row = k0 + 4 * k + lo;
+        const int64_t c = c0 + 2 * hi, n = row < p.r ? p.len - c : 0, x = base + (int64_t)min(row, p.r - 1) * p.len + c;
+        float2 g = make_float2(0.f, 0.f), m = g;
+        if (vec && n >= 2) {
+          g = __ldcg(reinterpret_cast<const float2*>(p.g + x));
+          m = __ldcg(reinterpret_cast<const float2*>(p.m + x));
+        } else {
+          if (n > 0) { g.x = __ldcg(p.g + x); m.x = __ldcg(p.m + x); }
+          if (n > 1) { g.y = __ldcg(p.g + x + 1); m.y = __ldcg(p.m + x + 1); }
+        }
+        f[0][k] = (double)muon_u(p, g.x, m.x);
+        f[1][k] = (double)muon_u(p, g.y, m.y);
       }
-      s_u[k][c] = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t c = c0 + 8 * e + hi;
+        const int64_t n = c < p.len ? p.r - k0 - KS * lo : 0, x = base + min(c, p.len - 1) * p.r + k0 + KS * lo;
+        float g[KS], m[KS];
+        load_run<KS>(p.g + x, n, vec, g);
+        load_run<KS>(p.m + x, n, vec, m);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) f[e][k] = (double)muon_u(p, g[k], m[k]);
+      }
+    }
+    __syncthreads();                               // the last part's products are done
+#pragma unroll 8
+    for (int e = threadIdx.x; e < 64 * 64; e += kApply64Threads) {
+      const int i = e / 64, j = e % 64;
+      const double v = i0 + i < p.rp && k0 + j < p.rp ? P[mat * sq + (int64_t)(i0 + i) * p.rp + k0 + j] : 0.0;
+      if (!kTall) {
+        s_p[i * kPitch + j] = v;
+      } else {
+        const int n = i / 16 * 2 + (i & 1), ib = i % 16 / 2;
+        s_p[(8 * ib + n) * kPitch + 4 * (j % KS) + j / KS] = v;
+      }
     }
     __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+    for (int ib = 0; ib < 8; ++ib) {
+      const double* s0 = s_p + (8 * ib + hi) * kPitch + lo;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) acc[q][w] = fma(s_p[ti + q][k], s_u[k][tc + w], acc[q][w]);
+      for (int k = 0; k < KS; ++k) {
+        const double x = s0[4 * k];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!kTall) dmma(d[ib][e], x, f[e][k]);
+          else dmma(d[ib][e], f[e][k], x);
+        }
+      }
+    }
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int i = i0 + ti + q;
-      const int64_t c = c0 + tc + w;
-      if (i >= p.r || c >= p.len) continue;
-      const int64_t at = muon_at(p, mat, i, c);
-      const float v = __fmaf_rn(p.keep, p.master[at], -__fmul_rn(p.step, (float)acc[q][w]));
-      p.master[at] = v;
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      p.w16[at] = *reinterpret_cast<const uint16_t*>(&h);
+  for (int r = 0; r < 8; ++r) {
+    // runs of four as in muon_apply64_kernel
+    int64_t at, have;
+    float w[4];
+    if (!kTall) {
+      const int row = i0 + 8 * r + hi;
+      const int64_t c = c0 + 4 * lo;
+      have = row < p.r ? p.len - c : 0;
+      at = base + (int64_t)min(row, p.r - 1) * p.len + c;
+    } else {
+      const int64_t c = c0 + 8 * (r & 1) + hi;
+      const int s = i0 + 16 * lo + 4 * (r >> 1);
+      have = c < p.len ? p.r - s : 0;
+      at = base + min(c, p.len - 1) * p.r + s;
     }
+    const bool v4 = kTall ? vec : (p.len & 3) == 0;
+    load_run<4>(p.master + at, have, v4, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = (float)(kTall ? d[(r & ~1) + i / 2][r & 1][i & 1] : d[r][i & 1][i / 2]);
+      w[i] = __fmaf_rn(p.keep, w[i], -__fmul_rn(p.step, x));
+    }
+    store_run<4>(p.master + at, have, v4, w);
+    if (v4 && have >= 4) {
+      const __nv_bfloat162 lo2 = __floats2bfloat162_rn(w[0], w[1]), hi2 = __floats2bfloat162_rn(w[2], w[3]);
+      *reinterpret_cast<uint2*>(p.w16 + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < have) {
+          const __nv_bfloat16 h = __float2bfloat16_rn(w[i]);
+          p.w16[at + i] = *reinterpret_cast<const uint16_t*>(&h);
+        }
+    }
+  }
 }
 
 }  // namespace qlora

@@ -579,7 +579,7 @@ struct FewGradArgs {
 constexpr int kFewGradThreads = 128;
 constexpr int kFewGradTokens = 32;
 
-__global__ void __launch_bounds__(kFewGradThreads) requests_few_grads_kernel(const FewGradArgs p) {
+__global__ void __launch_bounds__(kFewGradThreads, 2) requests_few_grads_kernel(const FewGradArgs p) {
   __shared__ __align__(16) float s_v[kFewGradTokens][16];
   __shared__ int s_tok[kFewGradTokens];
   griddep_wait();

@@ -908,16 +908,20 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
         if (!ok) break;
         tc_fence_after();
         if (mine) {
-          uint32_t v[NI][16];
+          constexpr int kTwo = NI < 2 ? NI : 2;
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-            if (16 * i < w.rc) tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * i, v[i]);
-          tmem_ld_wait();
+          for (int i0 = 0; i0 < NI; i0 += kTwo) {
+            uint32_t v[kTwo][16];
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-            if (16 * i < w.rc)
+            for (int i = 0; i < kTwo; ++i)
+              if (16 * (i0 + i) < w.rc) tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * (i0 + i), v[i]);
+            tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[i][j]);
+            for (int i = 0; i < kTwo; ++i)
+              if (16 * (i0 + i) < w.rc)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[i0 + i][j] += __uint_as_float(v[i][j]);
+          }
         }
         tc_fence_before();
         __syncwarp();
