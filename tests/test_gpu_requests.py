@@ -230,6 +230,32 @@ def test_on_another_stream():
         b.check_backward(r[2], r[3], r[4], r[1])
 
 
+def test_calls_on_several_streams_at_once():
+    """Chains on three streams, each with its own outputs and workspaces, give
+    what each gives alone."""
+    batches = [Batch(seed=20 + i, **CASES[n]) for i, n in enumerate(("training batch", "decoding, wide", "ranks past 64"))]
+
+    def chain(b, ws, stream=None):
+        got = []
+        for _ in range(6):
+            q4.lora_requests_plan(b.dev_lens, b.dev_ids, b.plan, stream=stream)
+            Y, U = q4.lora_requests_fwd(b.pool, b.plan, b.X, b.base_y, save=True, ws=ws, stream=stream)
+            got = [Y, U, *q4.lora_requests_bwd(b.pool, b.plan, b.X, U, b.dY, b.base_x, ws=ws, stream=stream)]
+        return got
+
+    wss = [q4.workspace(max(q4.lora_requests_fwd_workspace_bytes(b.pool, b.plan),
+                            q4.lora_requests_bwd_workspace_bytes(b.pool, b.plan))) for b in batches]
+    alone = [chain(b, ws) for b, ws in zip(batches, wss)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    for _ in range(3):
+        both = [chain(b, ws, s) for b, ws, s in zip(batches, wss, streams)]
+    torch.cuda.synchronize()
+    assert q4.qlora_get_device_status() == 0
+    for x, y in zip(alone, both):
+        assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
 def test_gradients_against_differences():
     """dA and dBt against differences of the fp32-valued loss sum(Y dY) formed
     from U and the factors: a directional derivative along the gradient."""
