@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(Poly64<NB>::kThreads, 1) muon_poly64_kernel(co
   extern __shared__ __align__(16) double s_mat[];
   double* H = s_mat + 4 * kMat;                    // 8 rows; R and Q of two rounds before it
   double* P[2] = {H + 8 * C::kPitch, H + 16 * C::kPitch};
-  __shared__ double s_inv;
+  __shared__ double s_trace[NB];
   __shared__ __align__(8) uint64_t s_bar[2];       // Q, R
   __shared__ int s_abort;
   const uint32_t q_bar = smem_u32(&s_bar[0]), r_bar = smem_u32(&s_bar[1]);
@@ -280,35 +280,57 @@ __global__ void __launch_bounds__(Poly64<NB>::kThreads, 1) muon_poly64_kernel(co
   const int q = (int)cluster_ctarank();
   const int64_t mat = blockIdx.x / NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hi = lane >> 2, lo = lane & 3;
-  // this CTA's 8 rows of the Gram matrix: the sum of the partials
-  const double* part = p.part + mat * parts * (int64_t)(kTiles * 64);
-  for (int e = threadIdx.x; e < 8 * C::kRp; e += C::kThreads) {
-    const int i = 8 * q + e / C::kRp, j = e % C::kRp;
-    // block and row within it of a short index
-    const int bi = kTall ? i % NB : i / 8, ri = kTall ? i / NB : i % 8, bj = kTall ? j % NB : j / 8, rj = kTall ? j / NB : j % 8;
-    const bool up = bi <= bj;
-    const int x = up ? bi : bj, y = up ? bj : bi;
-    const int at = (x * NB - x * (x - 1) / 2 + y - x) * 64 + (up ? ri * 8 + rj : rj * 8 + ri);
-    double v = 0.0;
-#pragma unroll 8
-    for (int k = 0; k < parts; ++k) v += part[k * kTiles * 64 + at];
-    const uint32_t to = smem_u32(s_mat + i * C::kPitch + j);
+  // the Gram matrix, whole in every CTA: sums of the partials in registers (two
+  // neighbours of an 8 x 8 block each), its trace, then R0 with the norm's factor
+  constexpr int kPairs = kTiles * 32, kEach = (kPairs + C::kThreads - 1) / C::kThreads;
+  const double2* part = reinterpret_cast<const double2*>(p.part + mat * parts * (int64_t)(kTiles * 64));
+  double2 sum[kEach];
 #pragma unroll
-    for (int c = 0; c < NB; ++c)
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(to, (uint32_t)c)), "d"(v) : "memory");
-  }
-  __syncwarp();
-  cluster_sync();
-  if (warp == 0) {
-    double t = 0.0;
-    for (int i = lane; i < C::kRp; i += 32) t += s_mat[i * C::kPitch + i];
+  for (int i = 0; i < kEach; ++i) sum[i] = make_double2(0.0, 0.0);
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    if (lane == 0) s_inv = 1.0 / (sqrt(t) + p.eps);
+    for (int i = 0; i < kEach; ++i) {
+      const int e = threadIdx.x + i * C::kThreads;
+      if (e < kPairs) {
+        const double2 v = __ldcg(part + k * kPairs + e);
+        sum[i].x += v.x;
+        sum[i].y += v.y;
+      }
+    }
+  double trace = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x + i * C::kThreads, ri = e % 32 / 4, rj = e % 4 * 2;
+    int x = 0, y = e / 32;
+    while (x < NB && y >= NB - x) { y -= NB - x; ++x; }
+    if (e < kPairs && y == 0) trace += ri == rj ? sum[i].x : ri == rj + 1 ? sum[i].y : 0.0;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) trace += __shfl_xor_sync(0xFFFFFFFFu, trace, o);
+  if (lane == 0) s_trace[warp] = trace;
   __syncthreads();
-  const double inv = s_inv;
-  for (int e = threadIdx.x; e < C::kRp * C::kRp; e += C::kThreads) s_mat[e / C::kRp * C::kPitch + e % C::kRp] *= inv * inv;
+  trace = 0.0;
+#pragma unroll
+  for (int w = 0; w < NB; ++w) trace += s_trace[w];
+  const double inv = 1.0 / (sqrt(trace) + p.eps);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = threadIdx.x + i * C::kThreads, ri = e % 32 / 4, rj = e % 4 * 2;
+    int x = 0, y = e / 32;
+    while (x < NB && y >= NB - x) { y -= NB - x; ++x; }
+    y += x;
+    if (e >= kPairs) break;
+    const double2 v = make_double2(sum[i].x * inv * inv, sum[i].y * inv * inv);
+    // short indices of the block's row and columns
+    const int r = kTall ? NB * ri + x : 8 * x + ri, c0 = kTall ? NB * rj + y : 8 * y + rj, c1 = kTall ? c0 + NB : c0 + 1;
+    s_mat[r * C::kPitch + c0] = v.x;
+    s_mat[r * C::kPitch + c1] = v.y;
+    if (x != y) {
+      s_mat[c0 * C::kPitch + r] = v.x;
+      s_mat[c1 * C::kPitch + r] = v.y;
+    }
+  }
   __syncthreads();
 
   // fragment addresses: this CTA's rows of R, Q; a warp's 8 columns (rows of a symmetric matrix)
