@@ -735,16 +735,20 @@ __device__ __forceinline__ GradPlace grad_place(const GradArgs& p, const GradUni
   return w;
 }
 
-// D[column][hi | mid | lo] (A operand: token rows, MN-major; B operand: V,
-// MN-major).  Only the hi part is moved to registers step by step: mid and lo
-// are 2^-8 of it and may be cut 2^8 times as often.
+// D[column][hi .. 64 | mid | lo] (A operand: token rows, MN-major; B operand: V,
+// MN-major): one MMA takes the three parts of V, so the token rows are read
+// from shared memory once.  The 256 columns are two accumulators; two steps
+// (128 tokens) go into the first, then into the second, and while one fills the
+// epilogue warps move the other to registers.  (With the parts in MMAs of their
+// own and the accumulators changing by step, operand reads beside the arriving
+// loads made a step 2,180 cycles.)
 template <int NI>                                // 16 of the rank each: 1 or 4
 __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_grads_kernel(
     const __grid_constant__ CUtensorMap box0, const __grid_constant__ CUtensorMap row0, const __grid_constant__ CUtensorMap terms0,
     const __grid_constant__ CUtensorMap box1, const __grid_constant__ CUtensorMap row1, const __grid_constant__ CUtensorMap terms1,
     const __grid_constant__ GradArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 5];
+  __shared__ __align__(8) uint64_t s_bar[2 * 8 + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ GradScan s_scan;
@@ -756,10 +760,9 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
   ring.full = smem_u32(&s_bar[0]);
   ring.empty = smem_u32(&s_bar[8]);
   ring.stages = p.stages;
-  const uint32_t acc_full = smem_u32(&s_bar[16]), acc_empty = smem_u32(&s_bar[18]);   // two each
-  const uint32_t rest_empty = smem_u32(&s_bar[20]);
-  // Tensor Memory: hi of each half in two alternating sets, then mid | lo of each half
-  const uint32_t rcw = (uint32_t)min(64, p.width);
+  // by half of the columns; Tensor Memory likewise
+  const uint32_t acc_full = smem_u32(&s_bar[16]), acc_empty = smem_u32(&s_bar[18]);
+  const uint32_t half_cols = 64u + 2u * (uint32_t)min(64, p.width);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(ring.full + 8u * i, 1);
@@ -767,9 +770,8 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8u * i, 1);
-      mbar_init(acc_empty + 8u * i, 8);
+      mbar_init(acc_empty + 8u * i, 4);
     }
-    mbar_init(rest_empty, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -846,46 +848,47 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
     // descriptors of stage 0: one thread issues, so an address costs it an addition
     const uint64_t xd0 = smem_desc_sw128(sbase, 8192, 1024), vd0 = smem_desc_sw128(sbase + 4u * 8192u, 8192, 1024);
     bool ok = true;
-    int n = 0, pieces = 0;                       // steps and pieces of units so far
+    int n[2] = {0, 0};                           // times that an accumulator was filled
     while (left > 0 && ok) {
       const GradPlace w = grad_place(p, g);
       const int step1 = (int)min((long long)g.steps, step0 + left);
       const int halves = w.cols - w.c0 > 128 ? 2 : 1;               // 128-column MMAs in use
-      const uint32_t id_hi = idesc_bf16_f32(128, w.rc, 1, 1), id_rest = idesc_bf16_f32(128, 2 * w.rc, 1, 1);
-      if (g.cnt > 0) {
-        // mid | lo of the last piece have been read
-        ok = mbar_wait_bounded(rest_empty, (uint32_t)((pieces & 1) ^ 1), abort_flag);
-        ++pieces;
-      }
-      for (int s = step0; s < step1 && g.cnt > 0 && ok; ++s, ++n) {
-        const int buf = n & 1;
-        ok = mbar_wait_bounded(acc_empty + 8u * buf, (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag) &&
-             mbar_wait_bounded(ring.full_bar(), ring.phase, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const int m = min(64, g.cnt - s * 64);
-        const uint32_t off = (uint32_t)(ring.at * p.stage_bytes) >> 4;
-        const uint64_t xd = xd0 + off, vd = vd0 + off;
-        const uint32_t more = s > step0 ? 1u : 0u;
-        const int ks = (m + 15) / 16;
-        for (int h = 0; h < halves; ++h) {
-          const uint32_t hi = tmem + (uint32_t)(buf * 2 + h) * rcw, rest = tmem + 4u * rcw + (uint32_t)h * 2u * rcw;
+      const uint32_t idesc = idesc_bf16_f32(128, 64 + 2 * w.rc, 1, 1);
+      for (int s = step0; s < step1 && g.cnt > 0 && ok; s += 2) {
+        const int two = min(2, step1 - s);
+        const int stage[2] = {ring.at, ring.at + 1 == p.stages ? 0 : ring.at + 1};
+        const uint32_t phase[2] = {ring.phase, ring.at + 1 == p.stages ? ring.phase ^ 1u : ring.phase};
+        for (int h = 0; h < halves && ok; ++h) {
+          ok = mbar_wait_bounded(acc_empty + 8u * h, (uint32_t)((n[h] & 1) ^ 1), abort_flag);
+          for (int i = 0; i < two && ok; ++i) {
+            if (h == 0) ok = mbar_wait_bounded(ring.full + 8u * stage[i], phase[i], abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const int ks = (min(64, g.cnt - (s + i) * 64) + 15) / 16;
+            const uint32_t off = (uint32_t)(stage[i] * p.stage_bytes) >> 4;
+            const uint64_t xd = xd0 + off + (uint64_t)(h * 1024), vd = vd0 + off;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < ks) {
-              umma_bf16(hi, xd + (uint64_t)(h * 1024 + k * 128), vd + (uint64_t)(k * 128), id_hi, k ? 1u : 0u);
-              umma_bf16(rest, xd + (uint64_t)(h * 1024 + k * 128), vd + (uint64_t)(512 + k * 128), id_rest, k ? 1u : more);
-            }
+            for (int k = 0; k < 4; ++k)
+              if (k < ks) umma_bf16(tmem + (uint32_t)h * half_cols, xd + (uint64_t)(k * 128), vd + (uint64_t)(k * 128), idesc, (i | k) ? 1u : 0u);
+            if (h == halves - 1) umma_commit(ring.empty + 8u * stage[i]);
+          }
+          if (ok) {
+            umma_commit(acc_full + 8u * h);
+            ++n[h];
+          }
         }
-        umma_commit(ring.empty_bar());
-        umma_commit(acc_full + 8u * buf);
         ring.next();
+        if (two == 2) ring.next();
       }
       left -= step1 - step0;
       step0 = 0;
       if (left > 0 && ok) grad_next_unit(p, g);
     }
-    if (!ok && n > 0) mbar_wait_bounded(acc_full + 8u * ((n - 1) & 1), (uint32_t)(((n - 1) >> 1) & 1), nullptr);
+    if (!ok) {
+      // MMAs already issued, before Tensor Memory is released
+      umma_commit(acc_full);
+      mbar_wait_bounded(acc_full, (uint32_t)(n[0] & 1), nullptr);
+    }
   } else if (warp >= 2) {
     const int quarter = warp & 3, h = (warp - 2) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -900,51 +903,28 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
-      for (int s = step0; s < step1 && g.cnt > 0; ++s, ++n) {
-        const int buf = n & 1;
-        ok = mbar_wait_bounded(acc_full + 8u * buf, (uint32_t)((n >> 1) & 1), abort_flag);
+      for (int s = step0; s < step1 && g.cnt > 0 && mine; s += 2, ++n) {
+        ok = mbar_wait_bounded(acc_full + 8u * h, (uint32_t)(n & 1), abort_flag);
         __syncwarp();
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (mine) {
-          constexpr int kTwo = NI < 2 ? NI : 2;
 #pragma unroll
-          for (int i0 = 0; i0 < NI; i0 += kTwo) {
-            uint32_t v[kTwo][16];
+        for (int i = 0; i < NI; ++i) {
+          if (16 * i >= w.rc) break;
+          uint32_t v[3][16];
+          const uint32_t t = lanes + (uint32_t)h * half_cols + 16u * i;
+          tmem_ld_32x32b_x16(t, v[0]);
+          tmem_ld_32x32b_x16(t + 64u, v[1]);
+          tmem_ld_32x32b_x16(t + 64u + (uint32_t)w.rc, v[2]);
+          tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < kTwo; ++i)
-              if (16 * (i0 + i) < w.rc) tmem_ld_32x32b_x16(lanes + (uint32_t)(buf * 2 + h) * rcw + 16u * (i0 + i), v[i]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < kTwo; ++i)
-              if (16 * (i0 + i) < w.rc)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) acc[i0 + i][j] += __uint_as_float(v[i][j]);
-          }
+          for (int j = 0; j < 16; ++j)
+            acc[i][j] += __uint_as_float(v[0][j]) + (__uint_as_float(v[1][j]) + __uint_as_float(v[2][j]));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty + 8u * buf);
-      }
-      if (g.cnt > 0 && ok) {
-        // mid | lo: the last step's barrier covers them
-        if (mine) {
-          const uint32_t t = lanes + 4u * rcw + (uint32_t)h * 2u * rcw;
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            if (16 * i >= w.rc) break;
-            uint32_t v[16], x[16];
-            tmem_ld_32x32b_x16(t + 16u * i, v);
-            tmem_ld_32x32b_x16(t + (uint32_t)w.rc + 16u * i, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[i][j] += __uint_as_float(v[j]) + __uint_as_float(x[j]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rest_empty);
+        if (lane == 0) mbar_arrive(acc_empty + 8u * h);
       }
       if (ok) {
         const bool whole = step0 == 0 && step1 == g.steps;
@@ -955,7 +935,7 @@ __global__ void __launch_bounds__(kReqGradThreads, NI == 1 ? 2 : 1) requests_gra
           out = (w.z ? p.dW[1] : p.dW[0]) + (int64_t)(g.ad.first + w.rc0) * ld + w.c0;
         } else {
           ld = kGradCols;
-          out = p.part + ((int64_t)blockIdx.x * 2 + (step0 > 0 ? 0 : 1)) * (int64_t)rcw * kGradCols;
+          out = p.part + ((int64_t)blockIdx.x * 2 + (step0 > 0 ? 0 : 1)) * (int64_t)min(64, p.width) * kGradCols;
           if (step0 == 0 && warp == 2 && lane == 0) {
             // the CTAs behind this one that have a part of the unit
             const long long end = total * (blockIdx.x + 1) / parts + g.steps - step1;
