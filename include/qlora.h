@@ -340,7 +340,7 @@ QLORA_API int lora_requests_plan(const int32_t* lens, const int32_t* adapters, c
  * Y[t] = bf16(base[t] + s_a U[t] B_a^T), U[t] = X[t] A_a^T in fp32, a the
  * adapter of token t; a token without one gets its base row.  X: T x k, base:
  * T x d (bf16; NULL counts as zero), Y: T x d, may be `base` itself but
- * must not overlap any input otherwise.  U_save: NULL, or T x width fp32, the
+ * must not overlap any input otherwise (Y == X is refused).  U_save: NULL, or T x width fp32, the
  * token's U for the backward (zero beyond its rank).  Rows of Y and U_save
  * behind the last request are left as they were.
  */
@@ -352,7 +352,8 @@ QLORA_API int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* 
 /*
  * Backward with dL/dY = dY (T x d) and G[t] = dY[t] B_a:
  *   dX[t] = bf16(base[t] + s_a G[t] A_a)   (base: the gradient through the
- *           shared projection, T x k; NULL counts as zero; may be dX itself)
+ *           shared projection, T x k; NULL counts as zero; may be dX itself,
+ *           which must not overlap X or dY: dX == X, dX == dY are refused)
  *   dA_a  = s_a sum_t G[t]^T X[t],   dBt_a = s_a sum_t U_saved[t]^T dY[t]
  * over the adapter's tokens.  dA: rows x k, dBt: rows x d, fp32, overwritten in
  * every adapter's rows: an adapter without tokens gets exact zeros, and so do

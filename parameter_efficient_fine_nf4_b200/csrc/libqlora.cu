@@ -1988,6 +1988,7 @@ int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* req, const
     return QLORA_ERR_MISALIGNED;
   const RequestsWs w = carve_requests(ws, *pool, *req, false);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  if (Y == X) return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(ensure_device());
   return requests_fwd(*pool, *req, X, base, Y, U_save, w, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -2008,6 +2009,7 @@ int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const
     return QLORA_ERR_MISALIGNED;
   const RequestsWs w = carve_requests(ws, *pool, *req, true);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  if (req->T > 0 && (dX == X || dX == dY)) return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(ensure_device());
   return requests_bwd(*pool, *req, X, U_saved, dY, base, dX, dA, dBt, w, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -2025,6 +2027,7 @@ int qlora_fwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora
   if (!aligned16(X) || !aligned16(Y) || !aligned16(U_save) || !aligned16(ws)) return QLORA_ERR_MISALIGNED;
   const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, false);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  if (Y == X) return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(ensure_device());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   QLORA_TRY(requests_base(false, q, X, req->T, Y, w.scales, st));
@@ -2047,6 +2050,7 @@ int qlora_bwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora
     return QLORA_ERR_MISALIGNED;
   const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, true);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
+  if (req->T > 0 && (dX == X || dX == dY)) return QLORA_ERR_INVALID_ARG;
   QLORA_TRY(ensure_device());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (req->T > 0) QLORA_TRY(requests_base(true, q, dY, req->T, dX, w.scales, st));

@@ -101,6 +101,9 @@ __device__ __forceinline__ void store_run(float* p, int64_t have, bool vec, cons
 // index NB (lane / 4) + b).  Loads are 16 bytes and nothing is staged.  The
 // warps of a cluster are then added in a fixed order; one partial per cluster.
 // part: [matrix][cluster][tile][8][8], tiles (i, j >= i) row by row.
+// Measured (alone, between two events, L2 flushed, some 4 us of each the events'):
+// 14.4 us for 64 x 4096, 30.7 us for two of 22016 x 64 (bound by the 64-bit
+// products), 14.4 us for eight of 16 x 11008.
 constexpr int kGram64Threads = 256;
 template <int NB>
 struct Gram64 {
@@ -217,7 +220,8 @@ __global__ void __launch_bounds__(kGram64Threads, 1) muon_gram64_kernel(const Mu
 // round: a CTA that runs ahead writes the next round's copy, and it gets no
 // further without this CTA's rows, which leave after its last read of the old
 // ones.  A product of 8 rows is one 8 x 8 block per warp; four of them a round
-// are about half of the time, the exchanges the rest.
+// are about half of the time, the exchanges the rest (as above: 22 us at rank
+// 64, 9.6 us at rank 16, five rounds).
 template <int NB>
 struct Poly64 {
   static constexpr int kRp = 8 * NB, kPitch = kRp + 4;     // pitch of 4 mod 16: fragments without bank conflicts
@@ -385,6 +389,7 @@ __global__ void __launch_bounds__(Poly64<NB>::kThreads, 1) muon_poly64_kernel(co
 // P's rows in shared memory.  Which k-step an index of the inner sum falls in,
 // and which column of a block a long-side (wide) or short-side (tall) index is,
 // is chosen so that every lane reads and writes runs of consecutive floats.
+// Measured (as above): 17 us for 64 x 4096, 26 us for two of 22016 x 64.
 constexpr int kApply64Threads = 128;
 template <int NB, bool kTall>
 __global__ void __launch_bounds__(kApply64Threads, 2) muon_apply64_kernel(const MuonArgs p) {
@@ -508,7 +513,8 @@ __global__ void __launch_bounds__(kApply64Threads, 2) muon_apply64_kernel(const 
 }
 
 // ------------------------------------------------------------ ranks above 64
-// m = mu m + g over all elements.
+// m = mu m + g over all elements.  Streaming: 7.9 us for 8192 x 128 alone between
+// two events (launch and events some 5 us of it).
 __global__ void __launch_bounds__(256) muon_momentum_kernel(float* __restrict__ m, const float* __restrict__ g, float mu,
                                                             int64_t count) {
   griddep_wait();
@@ -520,7 +526,8 @@ __global__ void __launch_bounds__(256) muon_momentum_kernel(float* __restrict__ 
 // One 64 x 64 block (i0, j0) of the partial Gram matrix of one chunk of the
 // long side: products and sums in 64 bits (the products of two 32-bit values
 // are exact).  A thread holds 4 x 4 sums; 32 long-side elements are staged at
-// a time.
+// a time.  Measured: 33 us for 8192 x 128, 74 us for 256 x 8192 (alone, between two
+// events).
 constexpr int kGramThreads = 256;
 constexpr int kGramStep = 32;
 constexpr int kGramPitch = 66;             // doubles per staged long-side element
@@ -597,7 +604,8 @@ __global__ void __launch_bounds__(kGramThreads, 2) muon_gram_kernel(const MuonAr
 }
 
 // R0 = (sum of the partials) / (|u|_F + eps)^2; P starts as I.  Four threads per
-// element take every fourth partial each, added in a fixed order.
+// element take every fourth partial each, added in a fixed order.  Measured: 20 us
+// for 8192 x 128 (86 partials), 33 us for 256 x 8192 (alone, between two events).
 __global__ void __launch_bounds__(256, 1) muon_norm_kernel(const MuonArgs p) {
   __shared__ double s_sum[256];
   griddep_wait();
@@ -633,7 +641,9 @@ __global__ void __launch_bounds__(256, 1) muon_norm_kernel(const MuonArgs p) {
 // 1: H = Q R (y < n) and the next P = Q P (y >= n, into `pout`), 2: R = Q H.
 // All factors are symmetric, so both operands are rows: a lane loads 16-byte
 // words (two k-steps, in any order), 128 of the inner sum in flight at once, and
-// nothing is staged.  Bound by the latency of one round of loads per launch.
+// nothing is staged.  Bound by the latency of one round of loads per launch: 14
+// launches of 5.9 us each (alone, between two events) in the 99 us of an 8192 x 128
+// step, 10 us each at 256 x 8192.
 constexpr int kSquareThreads = 128;
 __device__ __forceinline__ double2 load_ahead(const double2* p) {
   double2 v;
@@ -685,7 +695,8 @@ __global__ void __launch_bounds__(kSquareThreads, 1) muon_square_kernel(const Mu
 
 // x = P u and the update for 64 short-side rows (blockIdx.y) and 16 long-side
 // elements a warp: muon_apply64_kernel's fragments, the inner sum in parts of 64
-// with that part of P in shared memory.
+// with that part of P in shared memory.  Measured: 24 us for 8192 x 128, 84 us for
+// 256 x 8192 (alone, between two events).
 template <bool kTall>
 __global__ void __launch_bounds__(kApply64Threads, 2) muon_apply_kernel(const MuonArgs p, const double* P) {
   constexpr int kPitch = 68, KS = 16;

@@ -111,6 +111,26 @@ def test_values_do_not_leak_between_rows(name):
         assert torch.equal(dA[rows], cg[1][rows]) and torch.equal(dBt[rows], cg[2][rows])
 
 
+@pytest.mark.parametrize("lens", [[5, 9, 3], [150, 90, 40]])
+def test_infinite_tokens_leave_the_padding_rows_zero(lens):
+    b = Batch(72, 136, [5, 20], lens, [0, 1, -1], seed=9)
+    _, U = q4.lora_requests_fwd(b.pool, b.plan, b.X, b.base_y, save=True)
+    b.X[1, 3], b.dY[2, 7], b.X[lens[0] + 1, 70] = float("inf"), float("-inf"), float("nan")
+    _, dA, dBt = q4.lora_requests_bwd(b.pool, b.plan, b.X, U, b.dY)
+    assert not dA[:5].isfinite().all() and not dBt[:5].isfinite().all()
+    for pad in (slice(5, 16), slice(16 + 20, 16 + 32)):
+        assert not dA[pad].any() and not dBt[pad].any()
+
+
+def test_most_adapters_of_the_widest_rank():
+    ranks = [1] * 4095 + [256]
+    b = Batch(8, 16, ranks, [2, 3, 1], [4095, 7, 4094], seed=3, alphas=[float(r) for r in ranks])
+    Y, U = q4.lora_requests_fwd(b.pool, b.plan, b.X, b.base_y, save=True)
+    dX, dA, dBt = q4.lora_requests_bwd(b.pool, b.plan, b.X, U, b.dY, b.base_x)
+    b.check_forward(Y, U)
+    b.check_backward(dX, dA, dBt, U)
+
+
 def test_a_table_that_leaves_the_pool_counts_as_no_adapter():
     b = Batch(k=256, d=256, ranks=[8, 16], lens=[5, 200, 4], ids=[0, 1, 1], seed=8)
     want = q4.lora_requests_fwd(b.pool, b.plan, b.X, b.base_y)[0]

@@ -137,6 +137,12 @@ def test_call_refusals(q4):
     assert L.lora_requests_bwd(P, R, 16, None, 16, 16, 16, 16, 16, 16, 1 << 30, None) == 1
     assert L.lora_requests_bwd(P, R, 16, 16, 16, 16, 16, 16, 24, 16, 1 << 30, None) == 3
     assert L.lora_requests_bwd(P, R, 16, 16, 16, 16, 16, 16, 16, 16, 16, None) == 4
+    # outputs that are inputs read beside them
+    for Y, refused in ((16, True), (32, False)):
+        assert (L.lora_requests_fwd(P, R, 16, 16, Y, 16, 16, 1 << 30, None) == 1) == refused
+    for X, dY, dX, refused in ((16, 32, 16, True), (32, 16, 16, True), (32, 32, 16, False)):
+        got = L.lora_requests_bwd(P, R, X, 16, dY, dX, dX, 16, 16, 16, 1 << 30, None)
+        assert (got == 1) == refused
     assert L.lora_requests_max_tiles(4097, 1, 1) == 0 and L.lora_requests_max_tiles(1, 0, 1) == 0
     assert L.lora_requests_max_tiles(3, 2, 100) > 0
 
