@@ -38,6 +38,13 @@ CASES = {
     "ranks past 64": dict(k=512, d=640, ranks=[65, 96, 128, 130], lens=[40, 200, 100, 33, 140], ids=[0, 1, 2, 3, 1]),
     "many adapters": dict(k=128, d=128, ranks=[1 + i % 9 for i in range(200)], lens=[1 + i % 3 for i in range(150)],
                           ids=[(7 * i) % 200 for i in range(150)]),
+    "eight tokens per adapter": dict(k=72, d=136, ranks=[1 + i % 20 for i in range(255)], lens=[8] * 256,
+                                     ids=[i - 1 for i in range(256)]),
+    "one more than eight per adapter": dict(k=72, d=136, ranks=[1 + i % 20 for i in range(149)], lens=[9] + [8] * 149,
+                                            ids=[i - 1 for i in range(150)]),
+    "many adapters, nine tokens each": dict(k=264, d=136, ranks=[16, 70, 3] * 40, lens=[9] * 120, ids=list(range(120))),
+    "many adapters, one in use": dict(k=136, d=264, ranks=[24] * 100, lens=[5] * 100, ids=[42] * 100),
+    "more than 2048 tokens": dict(k=64, d=72, ranks=[8] * 300, lens=[7] * 300, ids=[(7 * i) % 301 - 1 for i in range(300)]),
     "one adapter, long": dict(k=1032, d=520, ranks=[24], lens=[700, 333], ids=[0, 0]),
     "training batch": dict(k=768, d=1024, ranks=[16, 64, 8], lens=[100, 250, 61, 300, 19, 77], ids=[0, 1, 2, 1, -1, 0]),
     "unused adapters": dict(k=256, d=256, ranks=[8, 16, 32, 8], lens=[90, 170], ids=[2, -1]),
