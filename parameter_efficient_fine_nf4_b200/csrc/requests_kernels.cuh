@@ -317,25 +317,36 @@ struct FewRing {
   }
 };
 
-// Stages of one factor for this CTA (one thread): for the first factor all
+// Stages of one factor for this CTA (one warp): for the first factor all
 // columns of 16 rows, then the next rows; for the second all rows of 256
 // columns.  Boxes of 64 columns x 16 rows, or 8 where the rank ends in a
-// stage's first 8; columns only up to the share's end.
+// stage's first 8; columns only up to the share's end.  A lane issues one box:
+// with one lane for all four, and its position by division, issuing took longer
+// than the warps' products.
 __device__ __forceinline__ bool few_produce(FewShared& s, FewRing& ring, int& issued, const CUtensorMap* w8,
                                             const CUtensorMap* w16, int first, int rank, int c0, int c1, bool rows_first) {
-  const int rb = (rank + kFewRows - 1) / kFewRows, cb = (c1 - c0 + kFewCols - 1) / kFewCols;
-  for (int i = 0; i < rb * cb; ++i) {
-    const int r = (rows_first ? i % rb : i / cb) * kFewRows, c = c0 + (rows_first ? i / rb : i % cb) * kFewCols;
+  const int lane = threadIdx.x & 31;
+  int r = 0, c = c0;
+  while (r < rank && c < c1) {
     const bool two = rank - r > 8;
     const int blocks = min(4, (c1 - c + 63) / 64);
     const uint32_t full = smem_u32(&s.full[ring.at]);
-    if (!mbar_wait_bounded(smem_u32(&s.empty[ring.at]), ring.phase ^ 1u, &s.abort_flag)) return false;
-    mbar_arrive_expect_tx(full, (uint32_t)(blocks * (two ? 2048 : 1024)));
-    const uint32_t dst = smem_u32(s.ring) + (uint32_t)(ring.at * kFewStageBytes);
-    const CUtensorMap* w = two ? w16 : w8;
-    for (int b = 0; b < blocks; ++b) tma_load_2d(dst + b * 2048u, w, full, c + 64 * b, first + r);
+    const bool ok = mbar_wait_bounded(smem_u32(&s.empty[ring.at]), ring.phase ^ 1u, &s.abort_flag);
+    if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(blocks * (two ? 2048 : 1024)));
+    if (lane < blocks)
+      tma_load_2d(smem_u32(s.ring) + (uint32_t)(ring.at * kFewStageBytes + lane * 2048), two ? w16 : w8, full, c + 64 * lane,
+                  first + r);
+    __syncwarp();
     ring.next();
     ++issued;
+    if (rows_first) {
+      r += kFewRows;
+      if (r >= rank) r = 0, c += kFewCols;
+    } else {
+      c += kFewCols;
+      if (c >= c1) c = c0, r += kFewRows;
+    }
   }
   return true;
 }
@@ -549,14 +560,12 @@ __global__ void __launch_bounds__(kFewThreads, 3) requests_few_kernel(const __gr
   const int k0 = min(p.K, q * kc), k1 = min(p.K, k0 + kc);
   const int n0 = min(p.N, q * nc), n1 = min(p.N, n0 + nc);
   if (threadIdx.x >= 32 * kFewWarps) {
-    if ((threadIdx.x & 31) == 0) {
-      FewRing ring;
-      int issued = 0;
-      if (!few_produce(s, ring, issued, &w1a, &w1b, ad.first, ad.rank, k0, k1, false) ||
-          !few_produce(s, ring, issued, &w2a, &w2b, ad.first, ad.rank, n0, n1, true))
-        for (int i = 0; i < min(issued, kFewStages); ++i)        // let copies in flight land
-          mbar_wait_bounded(smem_u32(&s.full[i]), (uint32_t)((issued - 1 - i) / kFewStages & 1), nullptr);
-    }
+    FewRing ring;
+    int issued = 0;
+    if (!few_produce(s, ring, issued, &w1a, &w1b, ad.first, ad.rank, k0, k1, false) ||
+        !few_produce(s, ring, issued, &w2a, &w2b, ad.first, ad.rank, n0, n1, true))
+      for (int i = 0; i < min(issued, kFewStages); ++i)        // let copies in flight land
+        mbar_wait_bounded(smem_u32(&s.full[i]), (uint32_t)((issued - 1 - i) / kFewStages & 1), nullptr);
   } else {
     few_consume(p, s, ad, tile, count, q, k0, k1, n0, n1);
   }
