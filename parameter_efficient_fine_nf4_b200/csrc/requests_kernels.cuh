@@ -239,9 +239,11 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // What is left is the time a stage takes the warps, so the products go through
 // m16n8k16 tensor instructions with the factor's rows (U) or columns (output)
 // as M and the tokens as N = 8: a tenth of the instructions of multiply-adds,
-// too small a product for tcgen05's 128 rows.  Measured: 12.5 us warm, 18.7 us
-// with L2 flushed, for 64 tokens of 48 adapters, 4096 x 4096; 7.4 us for 16
-// tokens, 256 x 256, of which the host's call is 5.  Sums over K are cut into at most
+// too small a product for tcgen05's 128 rows.  Measured: 12.0 us in
+// a chain, 20.5 us alone with L2 flushed, for 64 tokens of 48 adapters, 4096 x 4096; 3.3
+// us in a chain for 16 tokens, 256 x 256.  Of 9.5 us for 16 adapters of rank 64, 4.9
+// are the launch, the exchange and the output rows, 2.5 the ring's barriers, 1.8 the
+// products and 0.3 the loads.  Sums over K are cut into at most
 // 32 columns a warp and stage and added in fp32; for the output, U enters as
 // two bf16 terms (2^-16, far below the one rounding of the bf16 output).
 constexpr int kFewTile = 8;
