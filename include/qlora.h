@@ -46,7 +46,8 @@ typedef enum {
   QLORA_ERR_TIMEOUT = 6,           /* a device-side wait gave up (device status) */
   QLORA_ERR_NO_DEVICE = 7,         /* no sm_100 device is current */
   QLORA_ERR_EXCEEDS_STATIC_SCRATCH = 8, /* too large for qlora_nf4_quantize_noalloc */
-  QLORA_ERR_NCCL = 9               /* NCCL could not be loaded, or an NCCL call failed */
+  QLORA_ERR_NCCL = 9,              /* NCCL could not be loaded, or an NCCL call failed */
+  QLORA_ERR_OVERLAP = 10           /* an output overlaps an input, another output or the workspace */
 } qlora_status_t;
 
 /* A cudaStream_t passed as an opaque pointer (NULL = legacy default stream). */
@@ -340,9 +341,11 @@ QLORA_API int lora_requests_plan(const int32_t* lens, const int32_t* adapters, c
  * Y[t] = bf16(base[t] + s_a U[t] B_a^T), U[t] = X[t] A_a^T in fp32, a the
  * adapter of token t; a token without one gets its base row.  X: T x k, base:
  * T x d (bf16; NULL counts as zero), Y: T x d, may be `base` itself but
- * must not overlap any input otherwise (Y == X is refused).  U_save: NULL, or T x width fp32, the
+ * must not overlap any input otherwise.  U_save: NULL, or T x width fp32, the
  * token's U for the backward (zero beyond its rank).  Rows of Y and U_save
- * behind the last request are left as they were.
+ * behind the last request are left as they were.  Y == X is refused with
+ * QLORA_ERR_INVALID_ARG, other overlaps of Y, U_save and the workspace with
+ * X, base, the pool's factors or one another with QLORA_ERR_OVERLAP.
  */
 QLORA_API size_t lora_requests_fwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req);
 QLORA_API int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
@@ -352,13 +355,15 @@ QLORA_API int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* 
 /*
  * Backward with dL/dY = dY (T x d) and G[t] = dY[t] B_a:
  *   dX[t] = bf16(base[t] + s_a G[t] A_a)   (base: the gradient through the
- *           shared projection, T x k; NULL counts as zero; may be dX itself,
- *           which must not overlap X or dY: dX == X, dX == dY are refused)
+ *           shared projection, T x k; NULL counts as zero; may be dX itself)
  *   dA_a  = s_a sum_t G[t]^T X[t],   dBt_a = s_a sum_t U_saved[t]^T dY[t]
  * over the adapter's tokens.  dA: rows x k, dBt: rows x d, fp32, overwritten in
  * every adapter's rows: an adapter without tokens gets exact zeros, and so do
  * the rows between its rank and the next multiple of 16.  Rows that no
  * adapter owns are left as they were.  All sums are taken in a fixed order.
+ * dX == X and dX == dY are refused with QLORA_ERR_INVALID_ARG, other overlaps
+ * of an output or the workspace with X, U_saved, dY, base, the pool's factors
+ * or one another with QLORA_ERR_OVERLAP.
  */
 QLORA_API size_t lora_requests_bwd_workspace_bytes(const lora_pool_t* pool, const lora_requests_t* req);
 QLORA_API int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const uint16_t* X,
@@ -371,6 +376,7 @@ QLORA_API int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* 
  * Y and dX themselves.  Rows without an adapter, those behind the last
  * request among them, hold the base product (rounded to bf16 once; the others
  * a second time with their adapter's term).  pool's k and d are q's.
+ * Overlaps are refused as there.
  */
 QLORA_API size_t qlora_fwd_requests_workspace_bytes(const qlora_nf4_t* q, const lora_pool_t* pool,
                                                     const lora_requests_t* req);

@@ -1532,6 +1532,7 @@ const char* qlora_strerror(int s) {
     case QLORA_ERR_EXCEEDS_STATIC_SCRATCH:
       return "d*k exceeds the static scratch of qlora_nf4_quantize_noalloc (2^28 weights)";
     case QLORA_ERR_NCCL: return "NCCL unavailable or an NCCL call failed";
+    case QLORA_ERR_OVERLAP: return "an output overlaps another argument";
     default: return "unknown status";
   }
 }
@@ -1989,6 +1990,7 @@ int lora_requests_fwd(const lora_pool_t* pool, const lora_requests_t* req, const
   const RequestsWs w = carve_requests(ws, *pool, *req, false);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   if (Y == X) return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(check_fwd_overlap(*pool, *req, X, base, Y, U_save, ws, w.bytes));
   QLORA_TRY(ensure_device());
   return requests_fwd(*pool, *req, X, base, Y, U_save, w, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -2010,6 +2012,7 @@ int lora_requests_bwd(const lora_pool_t* pool, const lora_requests_t* req, const
   const RequestsWs w = carve_requests(ws, *pool, *req, true);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   if (req->T > 0 && (dX == X || dX == dY)) return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(check_bwd_overlap(*pool, *req, X, U_saved, dY, base, dX, dA, dBt, ws, w.bytes));
   QLORA_TRY(ensure_device());
   return requests_bwd(*pool, *req, X, U_saved, dY, base, dX, dA, dBt, w, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -2028,6 +2031,7 @@ int qlora_fwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora
   const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, false);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   if (Y == X) return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(check_fwd_overlap(*pool, *req, X, nullptr, Y, U_save, ws, w.bytes));
   QLORA_TRY(ensure_device());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   QLORA_TRY(requests_base(false, q, X, req->T, Y, w.scales, st));
@@ -2051,6 +2055,7 @@ int qlora_bwd_requests(const qlora_nf4_t* q, const lora_pool_t* pool, const lora
   const RequestsBaseWs w = carve_requests_base(ws, *q, *pool, *req, true);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   if (req->T > 0 && (dX == X || dX == dY)) return QLORA_ERR_INVALID_ARG;
+  QLORA_TRY(check_bwd_overlap(*pool, *req, X, U_saved, dY, nullptr, dX, dA, dBt, ws, w.bytes));
   QLORA_TRY(ensure_device());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (req->T > 0) QLORA_TRY(requests_base(true, q, dY, req->T, dX, w.scales, st));
