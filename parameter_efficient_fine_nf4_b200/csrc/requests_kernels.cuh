@@ -429,7 +429,8 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, cons
                      ? *reinterpret_cast<const uint32_t*>(p.base + (int64_t)tokb[i] * p.N + c + x2) : 0u;
   };
   load_base(n0);
-  if (p.csize > 1) ok = mbar_wait_bounded(smem_u32(&s.ready), 0, &s.abort_flag) && ok;
+  // (acquire at cluster scope: the sums read below were written by the other CTAs)
+  if (p.csize > 1) ok = mbar_wait_bounded<true>(smem_u32(&s.ready), 0, &s.abort_flag) && ok;
   __syncwarp();
   ok = __all_sync(0xFFFFFFFFu, ok);
   const int r16 = (ad.rank + 15) & ~15;
