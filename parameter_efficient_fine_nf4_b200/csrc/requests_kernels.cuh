@@ -243,9 +243,11 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // a chain, 20.5 us alone with L2 flushed, for 64 tokens of 48 adapters, 4096 x 4096; 3.3
 // us in a chain for 16 tokens, 256 x 256.  Of 9.5 us for 16 adapters of rank 64, 4.9
 // are the launch, the exchange and the output rows, 2.5 the ring's barriers, 1.8 the
-// products and 0.3 the loads.  Sums over K are cut into at most
-// 32 columns a warp and stage and added in fp32; for the output, U enters as
-// two bf16 terms (2^-16, far below the one rounding of the bf16 output).
+// products and 0.3 the loads.  The tensor core cuts what it adds up, so U leaves
+// the accumulator every 32 columns and is summed in registers, rounded to nearest:
+// in one accumulator, sums of one sign over 65536 columns were 2.5e-5 off, all
+// towards zero; now 1.4e-7 at worst and 2e-9 in the mean, at the same speed.  For the
+// output, U enters as two bf16 terms (2^-16, far below the one rounding of the bf16 output).
 constexpr int kFewTile = 8;
 constexpr int kFewWarps = 8;                   // consumers; one more warp produces
 constexpr int kFewThreads = 32 * (kFewWarps + 1);
@@ -373,7 +375,7 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, cons
   for (int g = 0; g < ad.rank; g += kFewGroup) {
     for (int r = g; r < min(ad.rank, g + kFewGroup) && ok; r += kFewRows) {
       const bool two = ad.rank - r > 8;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int c = k0; c < k1; c += kFewCols) {
         const int x0 = c + warp * 32 + lo * 8;
         const uint4 x = x0 < k1 ? __ldg(reinterpret_cast<const uint4*>(xrow + x0)) : make_uint4(0, 0, 0, 0);
@@ -384,16 +386,19 @@ __device__ __forceinline__ void few_consume(const FewArgs& p, FewShared& s, cons
           const uint8_t* st = s.ring + ring.at * kFewStageBytes + a_off;
           const uint4 w0 = *reinterpret_cast<const uint4*>(st);
           const uint4 w1 = two ? *reinterpret_cast<const uint4*>(st + 1024) : make_uint4(0, 0, 0, 0);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
           mma16816(acc, w0.x, w1.x, w0.y, w1.y, x.x, x.y);
           mma16816(acc, w0.z, w1.z, w0.w, w1.w, x.z, x.w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[j] += acc[j];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.empty[ring.at]));
         ring.next();
       }
       float* red = s.red + (warp * kFewGroup + (r - g) + hi) * kFewTile + 2 * lo;
-      *reinterpret_cast<float2*>(red) = make_float2(acc[0], acc[1]);
-      *reinterpret_cast<float2*>(red + 8 * kFewTile) = make_float2(acc[2], acc[3]);
+      *reinterpret_cast<float2*>(red) = make_float2(sum[0], sum[1]);
+      *reinterpret_cast<float2*>(red + 8 * kFewTile) = make_float2(sum[2], sum[3]);
     }
     named_bar_sync(1, 32 * kFewWarps);
     // the warps' sums of four tokens of a row, added in order, to every CTA
