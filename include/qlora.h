@@ -447,7 +447,9 @@ QLORA_API int lora_adam_step(float* master, uint16_t* weight_bf16, float* m, flo
  * or NULL for {3.4445, -4.7750, 2.0315}.  min(rows, cols) <= 256.  Arrays:
  * device, n rows cols elements, 16-byte aligned, updated in place (grad is
  * only read).  momentum in [0, 1), lr and weight_decay >= 0, eps > 0, 1 <=
- * steps <= 16.  A zero u leaves only the decay.
+ * steps <= 16 and |a|^(2 steps) <= 2^30 (8 steps with the usual coefficients):
+ * the iterations run on the Gram matrix, whose 64 bits hold no more than that
+ * where u has fewer directions than rows.  A zero u leaves only the decay.
  */
 QLORA_API size_t lora_muon_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 QLORA_API int lora_muon_step(float* master, uint16_t* weight_bf16, float* m, const float* grad, int64_t n, int64_t rows,

@@ -826,7 +826,8 @@ def lora_muon_step(master: torch.Tensor, weight_bf16: torch.Tensor, m: torch.Ten
                    stream=None) -> None:
     """One step that orthogonalises the momentum of each matrix of a stack
     (n x rows x cols, or one rows x cols), in place on (master, m) and the
-    bf16 copy; see qlora.h."""
+    bf16 copy; see qlora.h.  At most 8 steps with the usual coefs (in general
+    |coefs[0]| ** (2 * steps) <= 2 ** 30)."""
     if master.dim() not in (2, 3):
         raise ValueError("master: expected rows x cols or n x rows x cols")
     n = 1 if master.dim() == 2 else master.shape[0]

@@ -2076,6 +2076,9 @@ int lora_muon_step(float* master, uint16_t* weight_bf16, float* m, const float* 
     return QLORA_ERR_INVALID_ARG;
   for (int i = 0; coefs && i < 3; ++i)
     if (!std::isfinite(coefs[i])) return QLORA_ERR_INVALID_ARG;
+  const float usual[3] = {3.4445f, -4.7750f, 2.0315f};
+  if (!coefs) coefs = usual;
+  if (!muon_steps_hold(coefs[0], steps)) return QLORA_ERR_INVALID_ARG;
   if (!aligned16(master) || !aligned16(weight_bf16) || !aligned16(m) || !aligned16(grad) || !aligned16(ws))
     return QLORA_ERR_MISALIGNED;
   if (n == 0) return QLORA_OK;
@@ -2083,9 +2086,8 @@ int lora_muon_step(float* master, uint16_t* weight_bf16, float* m, const float* 
   const MuonWs w = carve_muon(ws, n, rows, cols);
   if (ws_bytes < w.bytes) return QLORA_ERR_WORKSPACE_TOO_SMALL;
   QLORA_TRY(ensure_device());
-  const float usual[3] = {3.4445f, -4.7750f, 2.0315f};
   return muon_step(master, weight_bf16, m, grad, n, rows, cols, lr, momentum, nesterov, scale, weight_decay, eps, steps,
-                   coefs ? coefs : usual, w, reinterpret_cast<cudaStream_t>(stream));
+                   coefs, w, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int qlora_get_device_status(qlora_stream_t stream, int* status) {

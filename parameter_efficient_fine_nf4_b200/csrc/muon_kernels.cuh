@@ -15,7 +15,8 @@
 // for P x0.  Small singular values grow some fivehundredfold, and P depends on
 // them through their squares, so R0 and the r x r products are held in 64
 // bits: rounding R0 to 32 bits alone would leave errors of 1e-3 in directions
-// a thousand times smaller than the largest.
+// a thousand times smaller than the largest.  64 bits hold a limited number of
+// rounds (muon_steps_hold); the host refuses more.
 //
 // "Wide" matrices (rows <= cols) use x x^T; tall ones the same formulas on
 // their transpose.  Element (i, c): i on the short side, c on the long one.

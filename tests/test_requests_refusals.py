@@ -84,3 +84,15 @@ def test_equal_addresses(q4):
         assert _bwd(q4, dict(a, dBt=a["dA"]), layer) == OVERLAP
         assert _bwd(q4, dict(a, dX=a["U"]), layer) == OVERLAP
     assert q4.strerror(OVERLAP) == "an output overlaps another argument"
+
+
+@pytest.mark.parametrize("coefs,most", [(None, 8), ((3.4445, -4.7750, 2.0315), 8), ((4.0848, -6.8946, 2.9270), 7),
+                                        ((-4.0848, 6.0, -2.0), 7), ((3.0, -3.2, 1.2), 9), ((2.0, -1.5, 0.5), 15),
+                                        ((0.5, 0.6, -0.1), 16)])
+def test_steps_that_the_gram_matrix_does_not_hold(q4, coefs, most):
+    """|a|^(2 steps) <= 2^30, and 16 at most; the steps that pass are refused for their workspace (4)."""
+    cs = None if coefs is None else (ctypes.c_float * 3)(*coefs)
+    for steps in range(1, 20):
+        got = q4.lib().lora_muon_step(16, 16, 16, 16, 1, 16, 256, 0.1, 0.9, 1, 1.0, 0.0, 1e-7, steps,
+                                      None if cs is None else ctypes.addressof(cs), 16, 16, None)
+        assert got == (4 if steps <= most else 1), steps
