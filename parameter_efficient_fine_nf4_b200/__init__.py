@@ -746,8 +746,9 @@ def lora_requests_bwd(pool: AdapterPool, plan: RequestPlan, X: torch.Tensor, U_s
     bp = None if base is None else _need_on(base, bf, (T, pool.k), dev, "base")
     with _On(dev, stream) as st:
         dX = torch.zeros(T, pool.k, dtype=bf, device=dev) if dX is None else dX
-        dA = torch.empty(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
-        dBt = torch.empty(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
+        # rows that no entry of the pool's tables names are not written: new gradients start at zero
+        dA = torch.zeros(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
+        dBt = torch.zeros(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
         dxp = _need_on(dX, bf, (T, pool.k), dev, "dX")
         dap = _need_on(dA, f32, (pool.rows, pool.k), dev, "dA")
         dbp = _need_on(dBt, f32, (pool.rows, pool.d), dev, "dBt")
@@ -805,8 +806,9 @@ def qlora_bwd_requests(q: NF4Weight, pool: AdapterPool, plan: RequestPlan, X: to
     gp = _need_on(dY, bf, (T, pool.d), dev, "dY")
     with _On(dev, stream) as st:
         dX = torch.empty(T, pool.k, dtype=bf, device=dev) if dX is None else dX
-        dA = torch.empty(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
-        dBt = torch.empty(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
+        # rows that no entry of the pool's tables names are not written: new gradients start at zero
+        dA = torch.zeros(pool.rows, pool.k, dtype=f32, device=dev) if dA is None else dA
+        dBt = torch.zeros(pool.rows, pool.d, dtype=f32, device=dev) if dBt is None else dBt
         dxp = _need_on(dX, bf, (T, pool.k), dev, "dX")
         dap = _need_on(dA, f32, (pool.rows, pool.k), dev, "dA")
         dbp = _need_on(dBt, f32, (pool.rows, pool.d), dev, "dBt")
