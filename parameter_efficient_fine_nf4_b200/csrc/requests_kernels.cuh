@@ -239,7 +239,7 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 // What is left is the time a stage takes the warps, so the products go through
 // m16n8k16 tensor instructions with the factor's rows (U) or columns (output)
 // as M and the tokens as N = 8: a tenth of the instructions of multiply-adds,
-// too small a product for tcgen05's 128 rows.  Measured: 12.0 us in
+// too small a product for tcgen05's 128 rows.  Measured: 12.2 us in
 // a chain, 20.5 us alone with L2 flushed, for 64 tokens of 48 adapters, 4096 x 4096; 3.3
 // us in a chain for 16 tokens, 256 x 256.  Of 9.5 us for 16 adapters of rank 64, 4.9
 // are the launch, the exchange and the output rows, 2.5 the ring's barriers, 1.8 the

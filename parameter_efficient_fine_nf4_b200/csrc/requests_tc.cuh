@@ -3,7 +3,8 @@
 //
 //   shrink:  V = s X A_a^T        (128 tokens x rank, K columns split over a cluster)
 //   expand:  Y = base + V Bt_a    (128 tokens x a range of columns)
-//   grads:   dA_a = V^T X         (256 columns x rank, tokens split over a cluster)
+//   grads:   dA_a = V^T X         (256 columns x rank, the tokens of all units cut into equal parts, one per CTA;
+//                                  a second kernel adds up the units that were cut)
 // The backward is the same three kernels with A and Bt, X and dY exchanged.
 //
 // V is a 32-bit value kept as three bf16 terms, v = hi + mid + lo (8 bits of
@@ -156,8 +157,11 @@ struct ShrinkArgs {
   uint16_t* V_in;               // ... whose terms (times the scale) are laid out as well
 };
 
-// X is streamed once; the factor's rows come from L2.  HBM-bound at ranks up
-// to 64; the split over the cluster only makes enough CTAs.  NI: 32 columns of
+// X is streamed once; the factor's rows come from L2; the split over the cluster
+// only makes enough CTAs.  Reading X is what has to be done, but no unit is near
+// its peak (46 % of DRAM at 8192 tokens of 11008 columns): set-up, the first loads
+// and the cluster's exchange are some 10 us of a launch, and above that a little over
+// one wave of CTAs leaves SMs idle at the end.  NI: 32 columns of
 // the rank per step of the epilogue's registers (width <= 32 NI).  Measured
 // (alone, between two events, L2 flushed): 4096 tokens of 4096 columns, ranks 8
 // to 64, 21 us; 16384 tokens of rank 64, 8192 columns 74 us (3.6 TB/s of X) and
@@ -404,7 +408,9 @@ __device__ __forceinline__ ExpandPiece expand_share(const ExpandArgs& p) {
 }
 
 // Streams base in and Y out, 64 columns of the tile's rows a stage, with a few
-// small MMAs (two per 16 of the rank) in between: HBM-bound.  Measured
+// small MMAs (two per 16 of the rank) in between.  Bound by DRAM on large batches, in
+// 128-byte pieces of rows (4.8 to 5.2 of the 6.5 TB/s of a copy); at 8192 tokens of
+// 4096 columns (35 us, 33 % of DRAM) by the first loads and the last stores.  Measured
 // (alone, between two events, L2 flushed): 75 us for 8192 tokens x 11008 columns of rank
 // 16 (4.8 TB/s in and out), 279 us for 16384 x 22016 of rank 64 (5.2 TB/s).  Two
 // CTAs an SM, so that one's loads run beside the other's epilogue.
